@@ -10,12 +10,17 @@ raise.
     o, lse = fwd_split(q, k, v)                   # same result, key range split across CTAs (S_q << S_k)
     dq, dk, dv = bwd(q, k, v, o, lse, do, causal=True)
 
-Inputs may also be CPU tensors: they are copied to the current device, the
+Serving and position rotation (``paged``): ``rope`` rotates q and k (and, inverse, their
+gradients); ``paged_append`` rotates new tokens into a paged cache, which
+``fwd_paged`` attends over.
+
+Inputs of fwd, bwd and fwd_bwd may also be CPU tensors: they are copied to the current device, the
 kernels run there, and the results are copied back to the host (the
 end-to-end path that the benchmark's ``e2e`` figure times).
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
 
@@ -23,9 +28,11 @@ import torch
 
 from . import _abi
 from ._abi import FwdOptions, load, status_string  # noqa: F401
+from .paged import PagedKV, Rotary, fwd_paged, fwd_paged_workspace_size, paged_append, rope  # noqa: F401
 
 __all__ = ["fwd", "fwd_qk8", "fwd_split", "fwd_split_count", "bwd", "fwd_bwd", "FwdBwdPipeline", "device_status", "set_wait_limit_ns", "exp2_poly_eval", "bwd_workspace_size",
-           "load", "status_string"]
+           "load", "status_string", "Rotary", "PagedKV", "rope", "paged_append", "fwd_paged",
+           "fwd_paged_workspace_size"]
 
 
 def _stream_ptr(stream, device=None) -> int:
@@ -238,31 +245,52 @@ def bwd(q, k, v, o, lse, do, causal: bool = False, scale: float | None = None, d
     return dq, dk, dv
 
 
+def _rotary_lengths(rotary, S_q, S_k):
+    if rotary is not None and S_q != S_k:
+        raise ValueError(f"rotary needs S_q == S_k (one position per token), got {S_q} and {S_k}")
+
+
 def fwd_bwd(q, k, v, do, causal: bool = False, scale: float | None = None, host_out: dict | None = None,
-            stream=None):
+            stream=None, rotary: Rotary | None = None, positions=None):
     """One training step of attention from host buffers: copy q, k, v, dO to the
     current device, run the forward and the backward there, and copy o, lse,
     dq, dk, dv back into ``host_out`` (pinned CPU tensors, allocated if None).
+    ``rotary``: q and k are rotated before the forward (``positions`` as in ``rope``,
+    host or device) and dq, dk are the gradients of the unrotated q and k.
     Returns the dict of host results."""
+    _rotary_lengths(rotary, q.shape[1], k.shape[1])
     dev = torch.device("cuda", torch.cuda.current_device())
-    qd, kd, vd, dod = (t.to(dev, non_blocking=True) for t in (q, k, v, do))
-    o, lse = fwd(qd, kd, vd, causal=causal, scale=scale, stream=stream)
-    dq, dk, dv = bwd(qd, kd, vd, o, lse, dod, causal=causal, scale=scale, stream=stream)
-    if host_out is None:
-        host_out = {}
-    res = {"o": o, "lse": lse, "dq": dq, "dk": dk, "dv": dv}
-    for name, t in res.items():
-        if name in host_out:
-            host_out[name].copy_(t, non_blocking=True)
-        else:
-            host_out[name] = t.to("cpu")
-    torch.cuda.current_stream().synchronize()
+    if stream is not None and stream.device != dev:
+        raise ValueError(f"stream is on {stream.device}, the current device is {dev}")
+    # the copies too run on the given stream, in order with the kernels
+    with contextlib.nullcontext() if stream is None else torch.cuda.stream(stream):
+        qd, kd, vd, dod = (t.to(dev, non_blocking=True) for t in (q, k, v, do))
+        qr, kr = qd, kd
+        if rotary is not None:
+            positions = None if positions is None else positions.to(dev)
+            qr, kr = rope(qd, kd, rotary=rotary, positions=positions)
+        o, lse = fwd(qr, kr, vd, causal=causal, scale=scale)
+        dq, dk, dv = bwd(qr, kr, vd, o, lse, dod, causal=causal, scale=scale)
+        if rotary is not None:
+            rope(dq, dk, rotary=rotary, positions=positions, inverse=True, q_out=dq, k_out=dk)
+        if host_out is None:
+            host_out = {}
+        res = {"o": o, "lse": lse, "dq": dq, "dk": dk, "dv": dv}
+        for name, t in res.items():
+            if name in host_out:
+                host_out[name].copy_(t, non_blocking=True)
+            else:
+                host_out[name] = t.to("cpu")
+        torch.cuda.current_stream().synchronize()
     return host_out
 
 
 class FwdBwdPipeline:
     """Attention training steps (forward + backward) from pinned host buffers,
     with the copies of one step overlapping the kernels of its neighbours.
+
+    ``rotary`` (with ``positions`` on the device as in ``rope``): q and k are rotated before
+    the forward, and dq, dk are the gradients of the unrotated q and k.
 
     Three streams: the inputs of a step (q, k, v, dO) go up on one copy stream,
     its kernels run on a compute stream, and its results (o, lse, dq, dk, dv)
@@ -278,7 +306,9 @@ class FwdBwdPipeline:
     """
 
     def __init__(self, B, S_q, S_k, H_q, H_kv, D, causal: bool = False, scale: float | None = None,
-                 depth: int = 2, device=None):
+                 depth: int = 2, device=None, rotary: Rotary | None = None, positions=None):
+        _rotary_lengths(rotary, S_q, S_k)
+        self.rotary, self.positions = rotary, positions
         self.dev = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
         self.causal = bool(causal)
         self.scale = 1.0 / math.sqrt(D) if scale is None else float(scale)
@@ -316,10 +346,16 @@ class FwdBwdPipeline:
                 s[name].copy_(t, non_blocking=True)
             s["uploaded"].record(self.up)
         self.compute.wait_event(s["uploaded"])
+        if self.rotary is not None:
+            rope(s["q"], s["k"], rotary=self.rotary, positions=self.positions, q_out=s["q"], k_out=s["k"],
+                 stream=self.compute)
         fwd(s["q"], s["k"], s["v"], causal=self.causal, scale=self.scale, out=s["o"], lse=s["lse"],
             stream=self.compute)
         bwd(s["q"], s["k"], s["v"], s["o"], s["lse"], s["do"], causal=self.causal, scale=self.scale,
             dq=s["dq"], dk=s["dk"], dv=s["dv"], workspace=s["ws"], stream=self.compute)
+        if self.rotary is not None:
+            rope(s["dq"], s["dk"], rotary=self.rotary, positions=self.positions, inverse=True, q_out=s["dq"],
+                 k_out=s["dk"], stream=self.compute)
         s["computed"].record(self.compute)
         self.down.wait_event(s["computed"])
         with torch.cuda.stream(self.down):

@@ -20,6 +20,7 @@ STATUS_NAMES = {
     4: "ATTN_ERR_CUDA",
     5: "ATTN_ERR_DEVICE_TIMEOUT",
     6: "ATTN_ERR_SCRATCH_TOO_SMALL",
+    7: "ATTN_ERR_BAD_INDEX",
 }
 
 # Every symbol include/attn.h declares (tests check the library exports all of them).
@@ -39,6 +40,10 @@ EXPORTED = (
     "attn_bwd",
     "attn_bwd_ex",
     "attn_bwd_noalloc",
+    "attn_rope",
+    "attn_paged_append",
+    "attn_fwd_paged",
+    "attn_fwd_paged_workspace_size",
     "attn_device_status",
     "attn_set_wait_limit_ns",
     "attn_exp2_poly_eval",
@@ -66,7 +71,25 @@ class BwdOptions(ctypes.Structure):
 
 _vp = ctypes.c_void_p
 _i = ctypes.c_int
+_ll = ctypes.c_longlong
 _f = ctypes.c_float
+
+
+class RotaryStruct(ctypes.Structure):
+    """attn_rotary_t"""
+
+    _fields_ = [("inv_freq", _vp), ("positions", _vp), ("n_freq", _i), ("n_axes", _i), ("section", _i * 4),
+                ("interleaved", _i)]
+
+
+class PagedKVStruct(ctypes.Structure):
+    """attn_paged_kv_t"""
+
+    _fields_ = [("k", _vp), ("v", _vp), ("e4m3", _i), ("n_pages", _i), ("page_size", _i), ("H_kv", _i), ("D", _i),
+                ("page_stride", _ll), ("token_stride", _ll), ("head_stride", _ll), ("k_scale", _f), ("v_scale", _f),
+                ("page_table", _vp), ("table_stride", _ll), ("max_pages", _i), ("seq_len", _vp), ("q_start", _vp),
+                ("n_seq", _i)]
+
 
 _SIGNATURES = {
     "attn_abi_version": (_i, []),
@@ -87,6 +110,10 @@ _SIGNATURES = {
     "attn_bwd": (_i, [_vp] * 10 + [_i, _i, _i, _i, _i, _i, _i, _f, _vp]),
     "attn_bwd_ex": (_i, [_vp] * 10 + [_i, _i, _i, _i, _i, _i, _i, _f, ctypes.POINTER(BwdOptions), _vp]),
     "attn_bwd_noalloc": (_i, [_vp] * 9 + [_i, _i, _i, _i, _i, _i, _i, _f, _vp]),
+    "attn_rope": (_i, [_vp] * 4 + [_ll, _i, _i, _i, _ll, _ll, _ll, _ll, _ll, _vp, _i, _vp]),
+    "attn_paged_append": (_i, [_vp] * 5 + [_i, _i, _ll, _ll, _ll, _vp, _vp]),
+    "attn_fwd_paged": (_i, [_vp] * 5 + [_i, _i, _ll, _i, _i, _f, _vp]),
+    "attn_fwd_paged_workspace_size": (ctypes.c_size_t, [_i, _i, _i]),
     "attn_device_status": (_i, [_vp]),
     "attn_set_wait_limit_ns": (None, [ctypes.c_ulonglong]),
     "attn_exp2_poly_eval": (_i, [_vp, _vp, ctypes.c_longlong, _vp]),

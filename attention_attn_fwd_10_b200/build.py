@@ -23,7 +23,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 LIB = os.path.join(HERE, "libattn.so")
 LIB_TIMELINE = os.path.join(HERE, "libattn_timeline.so")
-SOURCES = [os.path.join(HERE, "csrc", "attn_api.cu")]
+SOURCES = [os.path.join(HERE, "csrc", f) for f in ("attn_api.cu", "paged_api.cu")]
 DEPS = SOURCES + [
     os.path.join(HERE, "csrc", f)
     for f in sorted(os.listdir(os.path.join(HERE, "csrc")))

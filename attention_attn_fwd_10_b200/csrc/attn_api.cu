@@ -10,6 +10,7 @@
 #include <mutex>
 
 #include "../../include/attn.h"
+#include "api_internal.h"
 #include "bwd_kernels.cuh"
 #include "bwd_pair_kernel.cuh"
 #include "fwd_kernel.cuh"
@@ -47,10 +48,6 @@ constexpr int kBwdBhGroup = ATTN_BWD_BH_GROUP;
 
 constexpr int kNumSms = 148;     // B200
 constexpr int kMaxSplits = 128;  // key splits of the split-KV forward
-
-using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 
 EncodeTiledFn encode_fn() {
   static EncodeTiledFn fn = nullptr;
@@ -123,7 +120,7 @@ CUcontext current_ctx() {
   return c;
 }
 
-constexpr int kMaxDevices = 64;
+constexpr int kMaxDevices = kApiMaxDevices;
 
 // Per-device state of the library: device addresses of its __device__ symbols,
 // valid in the context they were looked up in.  A device reset (or anything else
@@ -469,6 +466,14 @@ int tc_split_count(int B, int H_q, int H_kv, int S_q, int S_k) {
 }
 
 }  // namespace
+
+EncodeTiledFn api_encode_tiled() { return encode_fn(); }
+int* api_status_ptr() { return status_ptr(); }
+unsigned long long api_wait_limit_ns() { return g_wait_limit_ns.load(); }
+cudaError_t api_smem_opt_in(const void* kernel, int bytes, CUcontext* seen) {
+  return smem_opt_in(kernel, bytes, seen);
+}
+
 }  // namespace attn
 
 using namespace attn;
@@ -487,6 +492,8 @@ const char* attn_status_string(attn_status_t s) {
     case ATTN_ERR_DEVICE_TIMEOUT: return "ATTN_ERR_DEVICE_TIMEOUT: a kernel abandoned a bounded wait";
     case ATTN_ERR_SCRATCH_TOO_SMALL:
       return "ATTN_ERR_SCRATCH_TOO_SMALL: the problem needs more scratch than attn_bwd_noalloc's fixed 32 MiB buffer";
+    case ATTN_ERR_BAD_INDEX:
+      return "ATTN_ERR_BAD_INDEX: a paged call met a page, length or token range outside its cache";
   }
   return "ATTN_ERR_UNKNOWN";
 }

@@ -54,7 +54,9 @@ typedef enum {
   ATTN_ERR_MISALIGNED = 3,     /* a tensor pointer is not 16-byte aligned */
   ATTN_ERR_CUDA = 4,           /* a CUDA runtime/driver call failed (no device, launch failure ...) */
   ATTN_ERR_DEVICE_TIMEOUT = 5, /* a kernel abandoned a bounded internal wait (see attn_device_status) */
-  ATTN_ERR_SCRATCH_TOO_SMALL = 6 /* attn_bwd_noalloc: the problem needs more than its fixed scratch */
+  ATTN_ERR_SCRATCH_TOO_SMALL = 6, /* attn_bwd_noalloc: the problem needs more than its fixed scratch */
+  ATTN_ERR_BAD_INDEX = 7       /* a paged call met a page, length or token range outside its cache
+                                  (see attn_device_status) */
 } attn_status_t;
 
 /* Version of this ABI (bumped on any incompatible change; 2: attn_bwd_options_t gained
@@ -198,6 +200,122 @@ int attn_fwd_split_count(int B, int H_q, int H_kv, int S_q, int S_k, int causal)
  * [n_splits, B, S_q, H_q, D] and lse_s [n_splits, B, H_q, S_q]; 0 for n_splits = 1
  * or invalid sizes. */
 size_t attn_fwd_split_workspace_size(int B, int H_q, int S_q, int D, int n_splits);
+
+/*
+ * Rotary positions.  The first 2 n_freq dims of each head are turned in pairs by
+ * the angle  a_i = position * inv_freq[i]  of pair i:
+ *     y_lo = x_lo cos a_i - x_hi sin a_i,   y_hi = x_hi cos a_i + x_lo sin a_i
+ * (inverse: -a_i, which is also the gradient's rule: dx = inverse(dy)); the other
+ * dims are passed on.  The angle is reduced in 64 bits, so it is as exact at position
+ * 10^6 as at 0; the rotation is computed in fp32 and rounded once.
+ *   inv_freq    : device, fp32 [n_freq], 4-byte aligned.
+ *   n_freq      : a multiple of 4, 4 <= n_freq <= D / 2.
+ *   n_axes      : 1 to 4 position axes (e.g. time, height, width).  Axis a gives the
+ *                 position of the section[a] frequencies after those of the axes
+ *                 before it; sections are >= 0 and sum to n_freq.
+ *   interleaved : 0 = pair i is dims (i, i + n_freq); 1 = dims (2i, 2i + 1).
+ *   positions   : device, int32 [n_axes, n_tokens], any value.  NULL (n_axes = 1 only):
+ *                 attn_rope takes the token's index modulo `period`, attn_paged_append
+ *                 the index of the token's key in its sequence.
+ */
+typedef struct {
+  const float* inv_freq;
+  const int* positions;
+  int n_freq;
+  int n_axes;
+  int section[4];
+  int interleaved;
+} attn_rotary_t;
+
+/*
+ * Turns q [n_tokens, H_q, D] into q_out and, where k is not NULL, k [n_tokens,
+ * H_k, D] into k_out, in one launch (bf16, D = 64 or 128).  Tokens are rows of
+ * H * D contiguous elements; consecutive tokens are *_stride elements apart (a
+ * multiple of 8, >= H * D), so a slice of a fused projection can be passed.  q_out may
+ * be q itself (with the same stride), k_out k; other overlaps are not allowed.  Backward
+ * pass: the same call on the gradients with inverse = 1.  `period` >= 1 is used
+ * with positions = NULL (S for BSHD tensors, n_tokens = B * S).
+ * n_tokens = 0 does nothing.  For S_q != S_k call it twice (k = NULL).
+ */
+attn_status_t attn_rope(const void* q, const void* k, void* q_out, void* k_out, long long n_tokens, int H_q, int H_k,
+                        int D, long long q_stride, long long k_stride, long long q_out_stride,
+                        long long k_out_stride, long long period, const attn_rotary_t* rotary, int inverse,
+                        void* stream);
+
+/*
+ * A paged key/value cache and the batch of sequences that a call works on.
+ *   k, v        : element (page, slot, head, d) at page * page_stride + slot *
+ *                 token_stride + head * head_stride + d, strides in elements, the
+ *                 same for k and v: [n_pages, page_size, H_kv, D] or [n_pages, H_kv,
+ *                 page_size, D] or a slice of such.  Strides are multiples of 16 bytes and
+ *                 no two elements may share a place (else ATTN_ERR_INVALID_ARG).
+ *   e4m3        : 0 = bf16; 1 = float8 e4m3, one byte per element, holding x / k_scale
+ *                 and x / v_scale (finite, > 0; both must be 1 for bf16).
+ *   page_size   : keys per page, a multiple of 16.
+ *   page_table  : device, int32, row b (table_stride elements apart, >= max_pages) lists
+ *                 sequence b's pages: key j is slot j % page_size of its page j / page_size.
+ *                 Sequences may share pages (a common prefix).
+ *   seq_len     : device, int32 [n_seq], keys of each sequence, its new tokens included.
+ *   q_start     : device, int32 [n_seq + 1], non-decreasing: sequence b's new tokens are
+ *                 rows q_start[b] .. q_start[b + 1] - 1 of q, k, v, o; they are its last
+ *                 keys.  A sequence may have none.  Rows before q_start[0] and from q_start[n_seq]
+ *                 on are left as they were in every output.
+ * The three index arrays are read on the device when the call runs (a captured call
+ * reads their contents at replay).  Entries that lead outside the cache -- a page not in
+ * [0, n_pages) among those a sequence needs, a length beyond max_pages * page_size,
+ * more new tokens than keys in an append, a token range outside [0, n_tokens] -- never cause an access
+ * out of range: the call records ATTN_ERR_BAD_INDEX in the device status word and the
+ * results of that sequence are undefined.
+ */
+typedef struct {
+  void* k;
+  void* v;
+  int e4m3;
+  int n_pages, page_size, H_kv, D;
+  long long page_stride, token_stride, head_stride;
+  float k_scale, v_scale;
+  const int* page_table;
+  long long table_stride;
+  int max_pages;
+  const int* seq_len;
+  const int* q_start;
+  int n_seq;
+} attn_paged_kv_t;
+
+/*
+ * Writes the new tokens' k and v (bf16 [n_tokens, H_kv, D], token strides k_stride,
+ * v_stride) into the cache, k turned by `rotary`, and their q (bf16 [n_tokens, H_q, D])
+ * turned into q_out (contiguous, or q itself when q_stride = H_q * D).  q NULL: only k and v; rotary NULL: no
+ * rotation (then q must be NULL).  e4m3: x / scale rounded to nearest, saturated at
+ * +-448, from the fp32 rotation's result (one rounding).  Two tokens that map to
+ * one slot (sequences that share their last page) leave either's value there.
+ */
+attn_status_t attn_paged_append(const attn_paged_kv_t* cache, const void* q, const void* k, const void* v, void* q_out,
+                                int n_tokens, int H_q, long long q_stride, long long k_stride, long long v_stride,
+                                const attn_rotary_t* rotary, void* stream);
+
+/*
+ * Attention of each sequence's new tokens over its paged keys: o [n_tokens, H_q, D]
+ * (bf16, contiguous) and lse [H_q, n_tokens] (fp32, natural log).  Causal: new token i of n of a
+ * sequence of L keys sees keys 0 .. L - n + i; else all L.  Rows that see no key get
+ * O = 0, lse = -inf.  One token per sequence (decoding) and chunks of a prompt may
+ * be mixed in one call.  Cache slots from a sequence's end on are never used,
+ * whatever they hold; the keys and values before it must be finite.  The e4m3 cache's
+ * products run on the 8-bit tensor-core path with q and the softmax weights as sums of
+ * two e4m3 terms, so they are as exact as with bf16.
+ *   q        : bf16, token stride q_stride elements (a multiple of 8, >= H_q * D).
+ *   H_q      : a multiple of the cache's H_kv, H_q / H_kv <= 128.
+ *   max_new  : the most new tokens of any sequence, as far as the caller knows: it
+ *              chooses the kernel, and any value gives the same result up to rounding.  0 = unknown.
+ *   workspace: device, 16-byte aligned, attn_fwd_paged_workspace_size(H_q, H_kv, D)
+ *              bytes; contents ignored, none kept.  Calls that may overlap need one each.
+ */
+attn_status_t attn_fwd_paged(const attn_paged_kv_t* cache, const void* q, void* o, float* lse, void* workspace,
+                             int n_tokens, int H_q, long long q_stride, int max_new, int causal, float scale,
+                             void* stream);
+
+/* Bytes of workspace attn_fwd_paged needs, whatever the lengths; 0 for invalid sizes. */
+size_t attn_fwd_paged_workspace_size(int H_q, int H_kv, int D);
 
 /*
  * Bytes of device workspace attn_bwd needs: an fp32 dQ accumulator
