@@ -9,7 +9,8 @@
 
 #include "../../include/attn.h"
 #include "api_internal.h"
-#include "paged_kernels.cuh"
+#include "paged_chunk_kernel.cuh"
+#include "paged_plan.cuh"
 #include "rotary_kernels.cuh"
 
 namespace attn {
@@ -123,6 +124,97 @@ attn_status_t check_cache(const attn_paged_kv_t* c, int n_tokens) {
   return ATTN_OK;
 }
 
+// The cache viewed as (D, H_kv, page_size, n_pages); boxes of one head, box_rows slots of one page, and
+// 128 bytes (or a whole e4m3 row of 64) across.
+bool make_cache_map(CUtensorMap* map, const attn_paged_kv_t* c, void* ptr, int box_rows) {
+  EncodeTiledFn enc = api_encode_tiled();
+  if (!enc) return false;
+  const long long eb = c->e4m3 ? 1 : 2;
+  auto bytes = [&](long long stride, int size) {  // a dim of one element may have any stride
+    return static_cast<cuuint64_t>((size > 1 ? stride : c->D) * eb);
+  };
+  const cuuint64_t dims[4] = {static_cast<cuuint64_t>(c->D), static_cast<cuuint64_t>(c->H_kv),
+                              static_cast<cuuint64_t>(c->page_size), static_cast<cuuint64_t>(c->n_pages)};
+  const cuuint64_t strides[3] = {bytes(c->head_stride, c->H_kv), bytes(c->token_stride, c->page_size),
+                                 bytes(c->page_stride, c->n_pages)};
+  const cuuint32_t across = static_cast<cuuint32_t>(c->e4m3 ? c->D : 64);
+  const cuuint32_t box[4] = {across, 1, static_cast<cuuint32_t>(box_rows), 1};
+  const cuuint32_t estride[4] = {1, 1, 1, 1};
+  return enc(map, c->e4m3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, ptr, dims, strides, box,
+             estride, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             across * eb == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// The token rows viewed as (D, H_q, tokens); boxes of one kv group's heads x `positions` tokens x 64 dims.
+bool make_q_map(CUtensorMap* map, const void* q, int n_tokens, int H_q, int D, long long q_stride, int group, int positions) {
+  EncodeTiledFn enc = api_encode_tiled();
+  if (!enc) return false;
+  const cuuint64_t dims[4] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(H_q), static_cast<cuuint64_t>(n_tokens), 1};
+  const cuuint64_t strides[3] = {static_cast<cuuint64_t>(D) * 2, static_cast<cuuint64_t>(q_stride) * 2,
+                                 static_cast<cuuint64_t>(q_stride) * 2};
+  const cuuint32_t box[4] = {64, static_cast<cuuint32_t>(group), static_cast<cuuint32_t>(positions), 1};
+  const cuuint32_t estride[4] = {1, 1, 1, 1};
+  return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(q), dims, strides, box, estride,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+constexpr int kPagedCtas = kNumSms;  // persistent: one CTA per SM
+
+// Workspace: the cut units' records, the pieces' log-sum-exps, their fp32 rows (two pieces per CTA).
+struct PagedWorkspace {
+  size_t l_off, o_off, bytes;
+};
+PagedWorkspace paged_workspace(int unit_rows, int D) {
+  auto up = [](size_t n) { return (n + 255) / 256 * 256; };
+  PagedWorkspace w;
+  const size_t rows = 2ull * kPagedCtas * unit_rows;
+  w.l_off = up(kPagedCtas * sizeof(int4));
+  w.o_off = w.l_off + up(rows * sizeof(float));
+  w.bytes = w.o_off + up(rows * D * sizeof(float));
+  return w;
+}
+
+// Joins the cut units: a programmatic dependent, so that its launch overlaps the attention's tail.
+template <int D, int TILE_ROWS>
+cudaError_t launch_merge(const PagedParams& p, cudaStream_t s) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(kPagedCtas - 1, static_cast<unsigned>((p.unit_rows + 7) / 8));
+  cfg.blockDim = dim3(256);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, paged_merge_kernel<D, TILE_ROWS>, p);
+}
+
+template <int D, bool KV8>
+cudaError_t launch_chunk(const attn_paged_kv_t* c, PagedParams p, void* workspace, cudaStream_t s) {
+  using L = ChunkLayout<D, KV8>;
+  p.tile_pos = 128 / p.group;
+  p.unit_pos = 2 * p.tile_pos;
+  p.unit_rows = 256;
+  p.min_steps = 4;
+  const PagedWorkspace w = paged_workspace(p.unit_rows, D);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  p.cut = reinterpret_cast<int4*>(ws);
+  p.l_part = reinterpret_cast<float*>(ws + w.l_off);
+  p.o_part = reinterpret_cast<float*>(ws + w.o_off);
+  CUtensorMap mq{}, mk, mv;
+  if (!KV8 && !make_q_map(&mq, p.q, p.n_tokens, p.H_q, D, p.q_stride, p.group, p.tile_pos)) return cudaErrorUnknown;
+  if (!make_cache_map(&mk, c, c->k, p.box_rows) || !make_cache_map(&mv, c, c->v, p.box_rows)) return cudaErrorUnknown;
+  auto kern = paged_chunk_kernel<D, KV8>;
+  static CUcontext seen[kApiMaxDevices] = {};
+  cudaError_t e = api_smem_opt_in(reinterpret_cast<const void*>(kern), L::SMEM_BYTES, seen);
+  if (e != cudaSuccess) return e;
+  kern<<<kPagedCtas, L::THREADS, L::SMEM_BYTES, s>>>(mq, mk, mv, p);
+  e = cudaGetLastError();
+  return e != cudaSuccess ? e : launch_merge<D, 128>(p, s);
+}
+
 }  // namespace
 }  // namespace attn
 
@@ -227,7 +319,7 @@ attn_status_t attn_paged_append(const attn_paged_kv_t* c, const void* q, const v
 
 size_t attn_fwd_paged_workspace_size(int H_q, int H_kv, int D) {
   if (H_q < 1 || H_kv < 1 || H_q % H_kv != 0 || H_q / H_kv > 128 || (D != 64 && D != 128)) return 0;
-  return 256;
+  return paged_workspace(256, D).bytes;
 }
 
 attn_status_t attn_fwd_paged(const attn_paged_kv_t* c, const void* q, void* o, float* lse, void* workspace,
@@ -247,8 +339,6 @@ attn_status_t attn_fwd_paged(const attn_paged_kv_t* c, const void* q, void* o, f
   p.q = static_cast<const __nv_bfloat16*>(q);
   p.o = static_cast<__nv_bfloat16*>(o);
   p.lse = lse;
-  p.k = c->k;
-  p.v = c->v;
   p.n_tokens = n_tokens;
   p.H_q = H_q;
   p.H_kv = c->H_kv;
@@ -258,9 +348,8 @@ attn_status_t attn_fwd_paged(const attn_paged_kv_t* c, const void* q, void* o, f
   p.page_size = c->page_size;
   p.max_pages = c->max_pages;
   p.n_seq = c->n_seq;
-  p.page_stride = c->page_stride;
-  p.token_stride = c->token_stride;
-  p.head_stride = c->head_stride;
+  while (p.box_shift < 7 && c->page_size % (2 << p.box_shift) == 0) ++p.box_shift;
+  p.box_rows = 1 << p.box_shift;
   p.table_stride = c->table_stride;
   p.page_table = c->page_table;
   p.seq_len = c->seq_len;
@@ -268,20 +357,14 @@ attn_status_t attn_fwd_paged(const attn_paged_kv_t* c, const void* q, void* o, f
   p.scale_log2 = static_cast<float>(static_cast<double>(scale) * c->k_scale * 1.4426950408889634);
   p.v_scale = c->v_scale;
   p.causal = causal;
+  p.wait_limit_ns = api_wait_limit_ns();
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const unsigned grid = static_cast<unsigned>((static_cast<long long>(n_tokens) * H_q + 7) / 8);
-  if (c->e4m3) {
-    if (c->D == 128)
-      paged_plain_kernel<128, __nv_fp8_e4m3><<<grid, 256, 0, s>>>(p);
-    else
-      paged_plain_kernel<64, __nv_fp8_e4m3><<<grid, 256, 0, s>>>(p);
-  } else {
-    if (c->D == 128)
-      paged_plain_kernel<128, __nv_bfloat16><<<grid, 256, 0, s>>>(p);
-    else
-      paged_plain_kernel<64, __nv_bfloat16><<<grid, 256, 0, s>>>(p);
-  }
-  return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+  cudaError_t e;
+  if (c->e4m3)
+    e = c->D == 128 ? launch_chunk<128, true>(c, p, workspace, s) : launch_chunk<64, true>(c, p, workspace, s);
+  else
+    e = c->D == 128 ? launch_chunk<128, false>(c, p, workspace, s) : launch_chunk<64, false>(c, p, workspace, s);
+  return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 
 }  // extern "C"

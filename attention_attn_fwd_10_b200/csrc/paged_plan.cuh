@@ -1,0 +1,338 @@
+// The work list of the paged attention, made on the device by each CTA.
+//
+// Lengths are read when the call runs, so the host cannot lay the work out.  A
+// unit is up to `unit_pos` new tokens of one sequence and the query heads of
+// one kv head; its steps are the 128-key blocks its last token sees (one step
+// where it sees none: its rows still get their zeros).  All units' steps form one
+// line, ordered by sequence, kv head, unit; CTA c takes the c-th of gridDim.x
+// equal stretches, so the loads are even whatever the lengths: a ragged batch, one long
+// sequence, chunks beside single tokens.  A unit cut by a stretch's end is
+// computed in pieces, each left in the workspace as fp32 rows normalized over
+// the piece's keys with their log-sum-exp, and joined by paged_merge_kernel.
+// Every CTA finds its stretch by itself from the index arrays (two passes of 32
+// sequences at a time): no planning launch and no state between calls.
+#pragma once
+
+#include "rotary_kernels.cuh"
+#include "sm100_common.cuh"
+
+namespace attn {
+
+struct PagedParams {
+  const __nv_bfloat16* q;
+  __nv_bfloat16* o;
+  float* lse;
+  int n_tokens, H_q, H_kv, group;
+  long long q_stride;
+  int n_pages, page_size, max_pages, n_seq;
+  int box_rows, box_shift;     // keys of one TMA box: the largest power of two that divides page_size, at most 128
+  long long table_stride;
+  const int *page_table, *seq_len, *q_start;
+  float scale_log2;            // scale * k_scale * log2(e)
+  float v_scale;
+  int causal;
+  int tile_pos, unit_pos;      // tokens of a tile, of a unit
+  int unit_rows;               // rows of a unit's partial result
+  int min_steps;               // least steps of a CTA's stretch
+  float* o_part;               // [2 gridDim.x, unit_rows, D]
+  float* l_part;               // [2 gridDim.x, unit_rows], base-2 log-sum-exp
+  int4* cut;                   // [2 gridDim.x]: the unit that stretch c starts inside of (CutUnit)
+  int* status;
+  uint64_t wait_limit_ns;
+};
+
+// One piece of a unit, as the roles of a CTA read it from shared memory.
+struct PagedItem {
+  int row0;     // the unit's first token row; -1: no more work
+  int n_pos;    // its tokens
+  int d0;       // last key its first token sees (causal)
+  int len;      // the sequence's keys
+  int head;     // kv head
+  int seq;
+  int j0;       // first key block of the piece
+  int nb0, nb1; // steps of tile 0 and tile 1
+  int n_loads;  // key blocks loaded, from j0 on
+  int dual;     // one tile holds every token: tile 0 takes the even, tile 1 the odd blocks of the piece
+  int slot;     // place of the partial result; -1: the piece is the whole unit
+};
+
+struct SeqWork {
+  int qs, n_new, len, diag, units;
+  bool bad;
+};
+
+__device__ __forceinline__ SeqWork seq_work(const PagedParams& p, int b) {
+  SeqWork w;
+  const int qs = p.q_start[b], qe = p.q_start[b + 1], len = p.seq_len[b];
+  const long long room = static_cast<long long>(p.max_pages) * p.page_size;
+  w.qs = max(0, min(qs, p.n_tokens));
+  w.n_new = max(0, min(qe, p.n_tokens) - w.qs);
+  w.len = static_cast<int>(max(0ll, min(static_cast<long long>(len), room)));
+  w.bad = w.qs != qs || qe < qs || qe > p.n_tokens || w.len != len;
+  w.diag = w.len - w.n_new;
+  w.units = (w.n_new + p.unit_pos - 1) / p.unit_pos;
+  return w;
+}
+
+// Key blocks that the tokens below position `end` (of the sequence's new ones) see.
+__device__ __forceinline__ int blocks_to(const PagedParams& p, const SeqWork& w, int end) {
+  const int last = p.causal ? min(min(end, w.n_new) - 1 + w.diag, w.len - 1) : w.len - 1;
+  return last < 0 ? 0 : (last >> 7) + 1;
+}
+__device__ __forceinline__ int unit_steps(const PagedParams& p, const SeqWork& w, int u) {
+  return max(1, blocks_to(p, w, (u + 1) * p.unit_pos));
+}
+
+__device__ __forceinline__ long long warp_sum(long long x) {
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) x += __shfl_xor_sync(0xffffffffu, x, off);
+  return x;
+}
+
+// Steps of one kv head of each lane's sequence (0 past the last): a lane counts few
+// units by itself; the warp counts a long chunk's together.
+__device__ __forceinline__ long long head_steps(const PagedParams& p, const SeqWork& w, int lane) {
+  long long mine = 0;
+  const bool many = w.units > 8;
+  if (!many)
+    for (int u = 0; u < w.units; ++u) mine += unit_steps(p, w, u);
+  for (unsigned left = __ballot_sync(0xffffffffu, many); left; left &= left - 1) {
+    const int src = __ffs(left) - 1;
+    SeqWork o;
+    o.n_new = __shfl_sync(0xffffffffu, w.n_new, src);
+    o.len = __shfl_sync(0xffffffffu, w.len, src);
+    o.diag = __shfl_sync(0xffffffffu, w.diag, src);
+    o.units = __shfl_sync(0xffffffffu, w.units, src);
+    long long part = 0;
+    for (int u = lane; u < o.units; u += 32) part += unit_steps(p, o, u);
+    part = warp_sum(part);
+    if (lane == src) mine = part;
+  }
+  return mine;
+}
+
+// A CTA's walk along its stretch, kept by the scheduler warp (the same in every lane).
+struct PagedWalk {
+  long long at, end;  // next step, end of the stretch
+  long long per;      // steps of a stretch
+  int b, head, u, blk;  // where `at` is: sequence, kv head, unit, block of the unit
+  SeqWork w;          // sequence b's
+};
+
+__device__ __forceinline__ void paged_walk_start(const PagedParams& p, PagedWalk& k, int cta, int n_ctas, int lane) {
+  long long total = 0;
+  for (int b0 = 0; b0 < p.n_seq; b0 += 32) {
+    SeqWork w{};
+    if (b0 + lane < p.n_seq) {
+      w = seq_work(p, b0 + lane);
+      if (w.bad && cta == 0) atomicExch(p.status, kDevBadIndex);
+    }
+    total += warp_sum(head_steps(p, w, lane)) * p.H_kv;
+  }
+  k.per = max((total + n_ctas - 1) / n_ctas, static_cast<long long>(p.min_steps));
+  k.at = min(k.per * cta, total);
+  k.end = min(k.at + k.per, total);
+  k.b = k.head = k.u = k.blk = 0;
+  if (k.at >= k.end) return;
+  long long before = 0;  // steps of the sequences before b0
+  for (int b0 = 0;; b0 += 32) {
+    SeqWork w{};
+    if (b0 + lane < p.n_seq) w = seq_work(p, b0 + lane);
+    const long long per_head = head_steps(p, w, lane);
+    long long upto = per_head * p.H_kv;  // inclusive prefix over the lanes
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const long long x = __shfl_up_sync(0xffffffffu, upto, off);
+      if (lane >= off) upto += x;
+    }
+    const unsigned past = __ballot_sync(0xffffffffu, before + upto > k.at);
+    if (past == 0 && b0 + 32 < p.n_seq) {
+      before += __shfl_sync(0xffffffffu, upto, 31);
+      continue;
+    }
+    const int src = past == 0 ? 31 : __ffs(past) - 1;  // (past == 0 does not happen: k.at < total)
+    const long long ph = max(1ll, __shfl_sync(0xffffffffu, per_head, src));
+    long long r = k.at - before - (__shfl_sync(0xffffffffu, upto, src) - ph * p.H_kv);
+    k.b = b0 + src;
+    k.head = static_cast<int>(r / ph);
+    r -= ph * k.head;
+    k.w = seq_work(p, min(k.b, p.n_seq - 1));
+    // the unit that holds step r of the head: 32 units at a time
+    for (int u0 = 0;; u0 += 32) {
+      const int steps = u0 + lane < k.w.units ? unit_steps(p, k.w, u0 + lane) : 0;
+      int sum = steps;
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1) {
+        const int x = __shfl_up_sync(0xffffffffu, sum, off);
+        if (lane >= off) sum += x;
+      }
+      const unsigned in = __ballot_sync(0xffffffffu, sum > r);
+      if (in == 0 && u0 + 32 < k.w.units) {
+        r -= __shfl_sync(0xffffffffu, sum, 31);
+        continue;
+      }
+      const int lu = in == 0 ? 31 : __ffs(in) - 1;
+      k.u = u0 + lu;
+      k.blk = static_cast<int>(r - (__shfl_sync(0xffffffffu, sum, lu) - __shfl_sync(0xffffffffu, steps, lu)));
+      break;
+    }
+    return;
+  }
+}
+
+// The next piece of the stretch (row0 = -1 when it is used up).
+__device__ __forceinline__ PagedItem paged_walk_next(const PagedParams& p, PagedWalk& k, int cta) {
+  PagedItem it{};
+  it.row0 = -1;
+  it.slot = -1;
+  if (k.at >= k.end) return it;
+  const int steps = unit_steps(p, k.w, k.u);
+  const int take = static_cast<int>(min(static_cast<long long>(steps - k.blk), k.end - k.at));
+  const int q0 = k.u * p.unit_pos;
+  it.row0 = k.w.qs + q0;
+  it.n_pos = min(p.unit_pos, k.w.n_new - q0);
+  it.d0 = q0 + k.w.diag;
+  it.len = k.w.len;
+  it.head = k.head;
+  it.seq = k.b;
+  it.j0 = k.blk;
+  const int j1 = k.blk + take;
+  const int all = min(blocks_to(p, k.w, q0 + p.unit_pos), j1);
+  it.dual = it.n_pos <= p.tile_pos;
+  if (it.dual) {
+    const int n = max(all - it.j0, 0);
+    it.nb0 = (n + 1) / 2;
+    it.nb1 = n / 2;
+    it.n_loads = n;
+  } else {
+    it.nb0 = max(min(blocks_to(p, k.w, q0 + p.tile_pos), j1) - it.j0, 0);
+    it.nb1 = max(all - it.j0, 0);
+    it.n_loads = max(it.nb0, it.nb1);
+  }
+  if (take < steps) it.slot = 2 * cta + (k.blk == 0 ? 1 : 0);
+  // advance
+  k.at += take;
+  k.blk += take;
+  if (k.blk == steps) {
+    k.blk = 0;
+    if (++k.u == k.w.units) {
+      k.u = 0;
+      if (++k.head == p.H_kv) {
+        k.head = 0;
+        if (k.at < k.end) {
+          do {
+            ++k.b;
+            k.w = seq_work(p, min(k.b, p.n_seq - 1));
+          } while (k.w.units == 0 && k.b < p.n_seq - 1);
+        }
+      }
+    }
+  }
+  return it;
+}
+
+// The unit that a stretch starts inside of, for the merge: its first token row, tokens, kv head and
+// last CTA, or row0 = -1 where the stretch starts a unit, is empty, or is not
+// the first one to start inside the unit (an earlier one merges it).
+__device__ __forceinline__ int4 paged_cut(const PagedParams& p, const PagedWalk& k, int cta) {
+  if (k.at >= k.end || k.blk == 0) return make_int4(-1, 0, 0, 0);
+  const long long start = k.at - k.blk;
+  if (start < (cta - 1) * k.per) return make_int4(-1, 0, 0, 0);
+  const int q0 = k.u * p.unit_pos;
+  const long long last = (start + unit_steps(p, k.w, k.u) - 1) / k.per;
+  return make_int4(k.w.qs + q0, min(p.unit_pos, k.w.n_new - q0), k.head, static_cast<int>(last));
+}
+
+// Joins the pieces of the units that were cut.  Block (c, y): rows 8 y .. 8 y + 7 of the unit
+// that stretch c + 1 starts inside of: pieces 2 c + 1 and 2 c', c' = c + 1 .. last.
+//   lse = log2 sum_s 2^(lse_s),   O = sum_s 2^(lse_s - lse) O_s
+// Pieces read by warps in turn when there are many (a long sequence over many
+// CTAs), else one row per warp; the order of the sums depends on the lengths only.
+template <int D, int TILE_ROWS>
+__global__ void __launch_bounds__(256) paged_merge_kernel(const PagedParams p) {
+  constexpr int PER = D / 32;
+  __shared__ __align__(16) float red_o[8][D];
+  __shared__ float red_m[8], red_l[8];
+  // a programmatic dependent of the attention kernel: waits for its results
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int c = blockIdx.x + 1;
+  const int4 cut = p.cut[c];
+  if (cut.x < 0) return;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int n = cut.w - c + 2;  // pieces
+  auto place = [&](int s) { return s == 0 ? 2 * c - 1 : 2 * (c + s - 1); };
+  const bool wide = n > 8;
+  for (int i = 0; i < (wide ? 8 : 1); ++i) {
+    const int r = blockIdx.y * 8 + (wide ? i : warp);
+    if (r >= p.unit_rows) break;
+    const int rr = r % TILE_ROWS;
+    const int pos = r / TILE_ROWS * p.tile_pos + rr / p.group;
+    const bool valid = rr < p.group * p.tile_pos && pos < cut.y;
+    if (!valid) continue;  // (the same for the whole block when wide)
+    const int first = wide ? warp : 0, step = wide ? 8 : 1;
+    float m = -INFINITY;
+    for (int s = first + lane * step; s < n; s += 32 * step)
+      m = fmaxf(m, p.l_part[static_cast<size_t>(place(s)) * p.unit_rows + r]);
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+    float acc[PER], sum = 0.f;
+#pragma unroll
+    for (int x = 0; x < PER; ++x) acc[x] = 0.f;
+    if (m > -INFINITY) {
+#pragma unroll 4
+      for (int s = first; s < n; s += step) {
+        const size_t at = static_cast<size_t>(place(s)) * p.unit_rows + r;
+        const float l = p.l_part[at];
+        const float wgt = exp2_mufu(l - m);  // 0 for a piece that saw no key
+        const float* src = p.o_part + at * D + lane * PER;
+        sum += wgt;
+#pragma unroll
+        for (int x = 0; x < PER / 2; ++x) {
+          const float2 v = reinterpret_cast<const float2*>(src)[x];
+          acc[2 * x] += wgt * v.x;
+          acc[2 * x + 1] += wgt * v.y;
+        }
+      }
+    }
+    if (wide) {
+#pragma unroll
+      for (int x = 0; x < PER; ++x) red_o[warp][lane * PER + x] = acc[x];
+      if (lane == 0) {
+        red_m[warp] = m;
+        red_l[warp] = sum;
+      }
+      __syncthreads();
+      if (warp == 0) {
+        float mm = red_m[0];
+#pragma unroll
+        for (int g = 1; g < 8; ++g) mm = fmaxf(mm, red_m[g]);
+        sum = 0.f;
+#pragma unroll
+        for (int x = 0; x < PER; ++x) acc[x] = 0.f;
+        if (mm > -INFINITY) {
+#pragma unroll
+          for (int g = 0; g < 8; ++g) {
+            const float wgt = exp2_mufu(red_m[g] - mm);
+            sum += wgt * red_l[g];
+#pragma unroll
+            for (int x = 0; x < PER; ++x) acc[x] += wgt * red_o[g][lane * PER + x];
+          }
+        }
+        m = mm;
+      }
+      __syncthreads();
+      if (warp != 0) continue;
+    }
+    const float inv = sum > 0.f ? 1.f / sum : 0.f;
+    const int h = cut.z * p.group + rr % p.group;
+    const long long row = static_cast<long long>(cut.x) + pos;
+    uint32_t* dst = reinterpret_cast<uint32_t*>(p.o + (row * p.H_q + h) * D + lane * PER);
+#pragma unroll
+    for (int x = 0; x < PER / 2; ++x) dst[x] = pack_bf16x2(acc[2 * x] * inv, acc[2 * x + 1] * inv);
+    if (lane == 0)
+      p.lse[static_cast<long long>(h) * p.n_tokens + row] =
+          sum > 0.f ? (m + log2f(sum)) * 0.69314718055994531f : -INFINITY;
+  }
+}
+
+}  // namespace attn

@@ -48,11 +48,13 @@ def gather(cache, pages, length, scale=1.0):
 
 
 def attend(q, k_cache, v_cache, page_table, seq_len, q_start, causal, scale, k_scale=1.0, v_scale=1.0):
-    """(o [tokens, H_q, D], lse [H_q, tokens], a [tokens, H_q, D]) with a = P |V|, the scale of the weights'
-    rounding errors in o; rows of no sequence are NaN."""
+    """(o [tokens, H_q, D], lse [H_q, tokens], a, f [tokens, H_q, D]) with a = P |V|, the scale in o of the
+    weights' relative errors, and f = max_j P_j x sum of the visible |V|, that of errors of a fixed part of the
+    largest weight; rows of no sequence are NaN."""
     T, H_q, D = q.shape
     o = np.full((T, H_q, D), np.nan)
     a = np.full((T, H_q, D), np.nan)
+    f = np.full((T, H_q, D), np.nan)
     lse = np.full((H_q, T), np.nan)
     for b in range(len(seq_len)):
         r = slice(q_start[b], q_start[b + 1])
@@ -60,11 +62,17 @@ def attend(q, k_cache, v_cache, page_table, seq_len, q_start, causal, scale, k_s
         if n == 0:
             continue
         if seq_len[b] == 0:
-            o[r], a[r], lse[:, r] = 0.0, 0.0, -np.inf
+            o[r], a[r], f[r], lse[:, r] = 0.0, 0.0, 0.0, -np.inf
             continue
         k = gather(k_cache, page_table[b], seq_len[b], k_scale)[None]
         v = gather(v_cache, page_table[b], seq_len[b], v_scale)[None]
         ob, lb = ref.forward(q[r][None], k, v, causal, scale)
         ab, _ = ref.forward(q[r][None], k, np.abs(v), causal, scale)
         o[r], a[r], lse[:, r] = ob[0], ab[0], lb[0]
-    return o, lse, a
+        seen = ref.visible(n, seq_len[b], causal)
+        for h in range(H_q):
+            g = h // (H_q // k.shape[2])
+            s = np.where(seen, scale * (ref.to_f64(q[r, h]) @ k[0, :, g].T), -np.inf).max(axis=1)
+            top = np.where(np.isneginf(s), 0.0, np.exp(np.where(np.isneginf(s), 0.0, s) - np.where(np.isneginf(s), 0.0, lb[0, h])))
+            f[r, h] = top[:, None] * (seen.astype(float) @ np.abs(v[0, :, g]))
+    return o, lse, a, f
