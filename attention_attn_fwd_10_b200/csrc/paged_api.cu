@@ -10,6 +10,7 @@
 #include "../../include/attn.h"
 #include "api_internal.h"
 #include "paged_chunk_kernel.cuh"
+#include "paged_few_kernel.cuh"
 #include "paged_plan.cuh"
 #include "rotary_kernels.cuh"
 
@@ -191,12 +192,13 @@ cudaError_t launch_merge(const PagedParams& p, cudaStream_t s) {
   return cudaLaunchKernelEx(&cfg, paged_merge_kernel<D, TILE_ROWS>, p);
 }
 
-template <int D, bool KV8>
-cudaError_t launch_chunk(const attn_paged_kv_t* c, PagedParams p, void* workspace, cudaStream_t s) {
-  using L = ChunkLayout<D, KV8>;
-  p.tile_pos = 128 / p.group;
-  p.unit_pos = 2 * p.tile_pos;
-  p.unit_rows = 256;
+// Lays the workspace out, encodes the maps and launches `kern` (one CTA per SM), then the merge.
+template <int D, bool KV8, int TILE_ROWS, typename L>
+cudaError_t launch_paged(void (*kern)(CUtensorMap, CUtensorMap, CUtensorMap, PagedParams), const attn_paged_kv_t* c,
+                         PagedParams p, int tiles, void* workspace, CUcontext* seen, cudaStream_t s) {
+  p.tile_pos = TILE_ROWS / p.group;
+  p.unit_pos = tiles * p.tile_pos;
+  p.unit_rows = tiles * TILE_ROWS;
   p.min_steps = 4;
   const PagedWorkspace w = paged_workspace(p.unit_rows, D);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
@@ -206,13 +208,24 @@ cudaError_t launch_chunk(const attn_paged_kv_t* c, PagedParams p, void* workspac
   CUtensorMap mq{}, mk, mv;
   if (!KV8 && !make_q_map(&mq, p.q, p.n_tokens, p.H_q, D, p.q_stride, p.group, p.tile_pos)) return cudaErrorUnknown;
   if (!make_cache_map(&mk, c, c->k, p.box_rows) || !make_cache_map(&mv, c, c->v, p.box_rows)) return cudaErrorUnknown;
-  auto kern = paged_chunk_kernel<D, KV8>;
-  static CUcontext seen[kApiMaxDevices] = {};
   cudaError_t e = api_smem_opt_in(reinterpret_cast<const void*>(kern), L::SMEM_BYTES, seen);
   if (e != cudaSuccess) return e;
   kern<<<kPagedCtas, L::THREADS, L::SMEM_BYTES, s>>>(mq, mk, mv, p);
   e = cudaGetLastError();
-  return e != cudaSuccess ? e : launch_merge<D, 128>(p, s);
+  return e != cudaSuccess ? e : launch_merge<D, TILE_ROWS>(p, s);
+}
+
+// The kernel by the rows that a sequence's new tokens make in a kv group (max_new, or the mean where it is not
+// known, times the group's heads): up to 32 as columns, more as tiles of 128 rows.
+template <int D, bool KV8>
+cudaError_t launch_attend(const attn_paged_kv_t* c, const PagedParams& p, int max_new, void* workspace, cudaStream_t s) {
+  static CUcontext seen[3][kApiMaxDevices] = {};
+  const long long rows = static_cast<long long>(max_new > 0 ? max_new : (p.n_tokens + p.n_seq - 1) / p.n_seq) * p.group;
+  if (rows <= 16)
+    return launch_paged<D, KV8, 16, FewLayout<D, KV8, 16>>(paged_few_kernel<D, KV8, 16>, c, p, 1, workspace, seen[0], s);
+  if (rows <= 32)
+    return launch_paged<D, KV8, 32, FewLayout<D, KV8, 32>>(paged_few_kernel<D, KV8, 32>, c, p, 1, workspace, seen[1], s);
+  return launch_paged<D, KV8, 128, ChunkLayout<D, KV8>>(paged_chunk_kernel<D, KV8>, c, p, 2, workspace, seen[2], s);
 }
 
 }  // namespace
@@ -354,16 +367,17 @@ attn_status_t attn_fwd_paged(const attn_paged_kv_t* c, const void* q, void* o, f
   p.page_table = c->page_table;
   p.seq_len = c->seq_len;
   p.q_start = c->q_start;
-  p.scale_log2 = static_cast<float>(static_cast<double>(scale) * c->k_scale * 1.4426950408889634);
+  p.scale_log2 = std::max(static_cast<float>(static_cast<double>(scale) * c->k_scale * 1.4426950408889634), 1.17549435e-38f);
   p.v_scale = c->v_scale;
   p.causal = causal;
   p.wait_limit_ns = api_wait_limit_ns();
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e;
   if (c->e4m3)
-    e = c->D == 128 ? launch_chunk<128, true>(c, p, workspace, s) : launch_chunk<64, true>(c, p, workspace, s);
+    e = c->D == 128 ? launch_attend<128, true>(c, p, max_new, workspace, s) : launch_attend<64, true>(c, p, max_new, workspace, s);
   else
-    e = c->D == 128 ? launch_chunk<128, false>(c, p, workspace, s) : launch_chunk<64, false>(c, p, workspace, s);
+    e = c->D == 128 ? launch_attend<128, false>(c, p, max_new, workspace, s)
+                    : launch_attend<64, false>(c, p, max_new, workspace, s);
   return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 

@@ -34,6 +34,7 @@
 
 #include "fwd_kernel.cuh"
 #include "paged_plan.cuh"
+#include "paged_tiles.cuh"
 #include "sm100_common.cuh"
 
 namespace attn {
@@ -93,20 +94,6 @@ struct ChunkLayout {
   static constexpr uint32_t HI = ROW_BYTES == 128 ? sdesc_sw128_hi(1024) : sdesc_sw64_hi(512);
 };
 
-// x = hi + lo, each a pair of e4m3 values (the first of a pair in the low byte).  fp16 holds the remainder
-// exactly: hi takes the leading four bits of at most eleven.
-__device__ __forceinline__ void split_e4m3x2(float x0, float x1, uint32_t& hi, uint32_t& lo) {
-  uint32_t h2, b2;
-  uint16_t h, l;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(h2) : "f"(x1), "f"(x0));
-  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(h) : "r"(h2));
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(b2) : "h"(h));
-  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(h2) : "r"(h2), "r"(b2));
-  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(l) : "r"(h2));
-  hi = h;
-  lo = l;
-}
-
 // A query row (bf16, D values in w) as hi and lo e4m3 terms, scaled by the power of two that puts its largest
 // element into [128, 256); written to row `row` of the swizzled tiles at dst and dst + lo_off (nowhere
 // where dst is null).  Returns scale_log2 with the power taken back out.
@@ -116,8 +103,8 @@ __device__ __forceinline__ float q_row_to_e4m3x2(const uint4* w, int row, uint8_
   uint32_t most = 0;  // the largest exponent field, in place in either half of a word
 #pragma unroll
   for (int i = 0; i < D / 2; ++i) most = max(most, max(x[i] & 0x7f80u, (x[i] >> 16) & 0x7f80u));
-  const int up = min(261 - static_cast<int>(most >> 7), 253);  // exponent field of the power
-  const float scale = __uint_as_float(static_cast<uint32_t>(up) << 23);
+  const uint32_t up = q_power(most);
+  const float scale = __uint_as_float(up << 23);
   if (dst != nullptr) {
 #pragma unroll
     for (int ch = 0; ch < D / 16; ++ch) {
@@ -137,28 +124,7 @@ __device__ __forceinline__ float q_row_to_e4m3x2(const uint4* w, int row, uint8_
       *reinterpret_cast<uint4*>(at + lo_off) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
     }
   }
-  return scale_log2 * __uint_as_float(static_cast<uint32_t>(254 - up) << 23);
-}
-
-// A producer warp's page numbers: lane l holds the page of box base + l of the current sequence.
-struct PageWindow {
-  int base;  // first box held; -1: none
-  int page;
-};
-
-// The page of box `box` of sequence `seq` (all lanes call with their own box, within one window of 32 boxes that
-// starts at a multiple of 32); -1 past the table or for an entry outside the cache (reported).
-__device__ __forceinline__ void window_load(const PagedParams& p, PageWindow& w, int seq, int base, int n_boxes, int lane) {
-  w.base = base;
-  w.page = -1;
-  const int box = base + lane;
-  if (box < n_boxes) {
-    const int page = p.page_table[seq * p.table_stride + (box << p.box_shift) / p.page_size];
-    if (page >= 0 && page < p.n_pages)
-      w.page = page;
-    else
-      atomicExch(p.status, kDevBadIndex);
-  }
+  return q_factor(scale_log2, up);
 }
 
 // p = 2^(s c - m) for 64 of a row's columns (exp_half's layout), as two e4m3 terms: words 0 .. 15 of pk hold the
@@ -250,25 +216,6 @@ __global__ void __launch_bounds__(ChunkLayout<D, KV8>::THREADS, 1)
   auto wait_item = [&](int u) { return mbar_wait(bar(L::B_ITEM_FULL + u % L::NI), (u / L::NI) & 1, ctl); };
   auto item_done = [&](int u) { return bar(L::B_ITEM_EMPTY + u % L::NI); };
 
-  // Loads block `blk` (128 keys) of a sequence's cache into shared memory at `dst`: box i of the block by lane i
-  // of the warp; returns the bytes it will bring.
-  const int boxes_log2 = 7 - p.box_shift;  // log2 of the boxes of a block
-  auto load_block = [&](const CUtensorMap* map, uint32_t dst, uint32_t full, PageWindow& win, const int seq, const int head,
-                        const int len, const int blk) {
-    const int n_boxes = (len + p.box_rows - 1) >> p.box_shift;
-    const int first = blk << boxes_log2;
-    if (win.base != (first & ~31)) window_load(p, win, seq, first & ~31, n_boxes, lane);
-    const int n = min(1 << boxes_log2, n_boxes - first);
-    if (lane == 0) mbar_arrive_expect_tx(full, static_cast<uint32_t>(n) * L::NBOX * p.box_rows * L::ROW_BYTES);
-    __syncwarp();
-    // lane: box lane % boxes of the block, column lane / boxes
-    const int i = lane & ((1 << boxes_log2) - 1), x = lane >> boxes_log2;
-    const int page = __shfl_sync(0xffffffffu, win.page, (first + i) & 31);
-    if (i < n && x < L::NBOX)
-      tma_load_4d(dst + x * L::BOX_BYTES + i * p.box_rows * L::ROW_BYTES, map, full, x * 64, head,
-                  ((first + i) << p.box_shift) % p.page_size, page);
-  };
-
   if (warp >= 8) setmaxnreg_dec<L::REG_OTHER>();
   if (warp == L::WARP_K) {
     // ===================== TMA producer: Q, K =====================
@@ -304,7 +251,8 @@ __global__ void __launch_bounds__(ChunkLayout<D, KV8>::THREADS, 1)
         const int s = kn % L::KST;
         if (kn >= L::KST && !(ok = __all_sync(0xffffffffu, mbar_wait(bar(L::B_K_EMPTY + s), ((kn / L::KST) - 1) & 1, ctl))))
           break;
-        load_block(&tm_k, sbase + L::K_OFF + s * L::KV_BYTES, bar(L::B_K_FULL + s), win, seq, head, len, j0 + j);
+        load_block<L::NBOX, L::ROW_BYTES>(p, &tm_k, sbase + L::K_OFF + s * L::KV_BYTES, bar(L::B_K_FULL + s), win, seq, head,
+                                           len, j0 + j, lane);
         ++kn;
       }
     }
@@ -333,19 +281,12 @@ __global__ void __launch_bounds__(ChunkLayout<D, KV8>::THREADS, 1)
         const uint32_t dst = sbase + L::V_OFF + s * L::KV_BYTES;
         const int live = len - (j0 + j) * L::BN;  // keys of the block that the sequence has
         if (live >= L::BN) {
-          load_block(&tm_v, dst, bar(L::B_V_FULL + s), win, seq, head, len, j0 + j);
+          load_block<L::NBOX, L::ROW_BYTES>(p, &tm_v, dst, bar(L::B_V_FULL + s), win, seq, head, len, j0 + j, lane);
         } else {
-          load_block(&tm_v, dst, bar(L::B_V_RAW), win, seq, head, len, j0 + j);
+          load_block<L::NBOX, L::ROW_BYTES>(p, &tm_v, dst, bar(L::B_V_RAW), win, seq, head, len, j0 + j, lane);
           const bool landed = __all_sync(0xffffffffu, mbar_wait(bar(L::B_V_RAW), raw_n & 1, ctl));
           if (landed) {
-            // whole rows: the swizzle moves 16-byte chunks within a row only
-            const uint4 zero = make_uint4(0, 0, 0, 0);
-#pragma unroll
-            for (int x = 0; x < L::NBOX; ++x)
-              for (int c = live * (L::ROW_BYTES / 16) + lane; c < L::BOX_BYTES / 16; c += 32)
-                *reinterpret_cast<uint4*>(sptr + (dst - sbase) + x * L::BOX_BYTES + c * 16) = zero;
-            fence_proxy_async_smem();
-            __syncwarp();
+            zero_tail<L::NBOX, L::ROW_BYTES>(sptr + (dst - sbase), live, lane);
             if (lane == 0) mbar_arrive(bar(L::B_V_FULL + s));
           }
           ++raw_n;

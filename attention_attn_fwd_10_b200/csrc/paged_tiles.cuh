@@ -1,0 +1,87 @@
+// Loading a paged cache's 128-key blocks, and e4m3 pairs: shared by the paged attention kernels.
+#pragma once
+
+#include "paged_plan.cuh"
+#include "sm100_common.cuh"
+
+namespace attn {
+
+// x = hi + lo, each a pair of e4m3 values (the first of a pair in the low byte).  fp16 holds the remainder
+// exactly: hi takes the leading four bits of at most eleven.
+__device__ __forceinline__ void split_e4m3x2(float x0, float x1, uint32_t& hi, uint32_t& lo) {
+  uint32_t h2, b2;
+  uint16_t h, l;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(h2) : "f"(x1), "f"(x0));
+  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(h) : "r"(h2));
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(b2) : "h"(h));
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(h2) : "r"(h2), "r"(b2));
+  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(l) : "r"(h2));
+  hi = h;
+  lo = l;
+}
+
+// A query row's power of two for its e4m3 terms: `most` is the largest element's exponent field as it sits in a bf16
+// (bits 7 .. 14); the power (as an fp32 exponent field) puts that element into [128, 256).  At most 2^73: rows
+// below 2^-66 have scores of 0 all the same, and the factor taken back out stays a normal number.
+__device__ __forceinline__ uint32_t q_power(uint32_t most) {
+  return static_cast<uint32_t>(min(261 - static_cast<int>(most >> 7), 200));
+}
+__device__ __forceinline__ float q_factor(float scale_log2, uint32_t power) {
+  return fmaxf(scale_log2 * __uint_as_float((254u - power) << 23), 1.17549435e-38f);
+}
+
+// A producer warp's page numbers: lane l holds the page of box base + l of the current sequence.
+struct PageWindow {
+  int base;  // first box held; -1: none
+  int page;
+};
+
+// The page of box `box` of sequence `seq` (all lanes call with their own box, within one window of 32 boxes that
+// starts at a multiple of 32); -1 past the table or for an entry outside the cache (reported).
+__device__ __forceinline__ void window_load(const PagedParams& p, PageWindow& w, int seq, int base, int n_boxes, int lane) {
+  w.base = base;
+  w.page = -1;
+  const int box = base + lane;
+  if (box < n_boxes) {
+    const int page = p.page_table[seq * p.table_stride + (box << p.box_shift) / p.page_size];
+    if (page >= 0 && page < p.n_pages)
+      w.page = page;
+    else
+      atomicExch(p.status, kDevBadIndex);
+  }
+}
+
+// Loads block `blk` (128 keys) of a sequence's cache into shared memory at `dst`: box i of the block by lane i of
+// the warp (lane i + boxes: its second 128-byte column); `full` completes when all of them have landed.
+// NBOX columns of ROW_BYTES; boxes wholly past the sequence's end are left out.
+template <int NBOX, int ROW_BYTES>
+__device__ __forceinline__ void load_block(const PagedParams& p, const CUtensorMap* map, uint32_t dst, uint32_t full,
+                                           PageWindow& win, int seq, int head, int len, int blk, int lane) {
+  const int boxes_log2 = 7 - p.box_shift;  // of a block
+  const int n_boxes = (len + p.box_rows - 1) >> p.box_shift;
+  const int first = blk << boxes_log2;
+  if (win.base != (first & ~31)) window_load(p, win, seq, first & ~31, n_boxes, lane);
+  const int n = min(1 << boxes_log2, n_boxes - first);
+  if (lane == 0) mbar_arrive_expect_tx(full, static_cast<uint32_t>(n) * NBOX * p.box_rows * ROW_BYTES);
+  __syncwarp();
+  const int i = lane & ((1 << boxes_log2) - 1), x = lane >> boxes_log2;
+  const int page = __shfl_sync(0xffffffffu, win.page, (first + i) & 31);
+  if (i < n && x < NBOX)
+    tma_load_4d(dst + x * 128 * ROW_BYTES + i * p.box_rows * ROW_BYTES, map, full, x * 64, head,
+                ((first + i) << p.box_shift) % p.page_size, page);
+}
+
+// Writes zeros over the rows of a landed block that lie past the sequence's end (`live` keys are the sequence's), by
+// the whole warp, visible to the tensor cores.  Whole rows: the swizzle moves 16-byte chunks within a row only.
+template <int NBOX, int ROW_BYTES>
+__device__ __forceinline__ void zero_tail(uint8_t* tile, int live, int lane) {
+  const uint4 zero = make_uint4(0, 0, 0, 0);
+#pragma unroll
+  for (int x = 0; x < NBOX; ++x)
+    for (int c = live * (ROW_BYTES / 16) + lane; c < 128 * ROW_BYTES / 16; c += 32)
+      *reinterpret_cast<uint4*>(tile + x * 128 * ROW_BYTES + c * 16) = zero;
+  fence_proxy_async_smem();
+  __syncwarp();
+}
+
+}  // namespace attn
