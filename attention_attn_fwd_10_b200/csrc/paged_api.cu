@@ -45,6 +45,25 @@ attn_status_t set_rotary(RotaryParams* p, const attn_rotary_t* r, int D, bool in
   return ATTN_OK;
 }
 
+// Launches a kernel as a programmatic dependent of the one before it on the stream: its blocks may start as that
+// one's last blocks finish, and wait on the device (griddepcontrol.wait) before they touch memory.  A layer's
+// append, attention and merge are short kernels in a row, whose launch and set-up overlap so.
+template <typename... Params, typename... Args>
+cudaError_t launch_dependent(void (*kern)(Params...), dim3 grid, unsigned threads, size_t smem, cudaStream_t s,
+                             const Args&... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
 template <int D, int VEC, bool INTERLEAVED, bool PAGED, bool E4M3>
 cudaError_t launch_rotary(RotaryParams p, cudaStream_t s) {
   constexpr int ITEMS = 4;
@@ -62,9 +81,8 @@ cudaError_t launch_rotary(RotaryParams p, cudaStream_t s) {
   const long long gx = (p.n_tokens + tok - 1) / tok;
   const int gy = (p.n_heads + hpc - 1) / hpc;
   if (gx > 2147483647ll || gy > 65535) return cudaErrorInvalidConfiguration;
-  rotary_kernel<D, VEC, ITEMS, INTERLEAVED, PAGED, E4M3>
-      <<<dim3(static_cast<unsigned>(gx), static_cast<unsigned>(gy)), kRotThreads, 0, s>>>(p);
-  return cudaGetLastError();
+  return launch_dependent(rotary_kernel<D, VEC, ITEMS, INTERLEAVED, PAGED, E4M3>,
+                          dim3(static_cast<unsigned>(gx), static_cast<unsigned>(gy)), kRotThreads, 0, s, p);
 }
 
 // 16-byte chunks need frequencies in eights; else (rotated dims such as 24) 8-byte ones.
@@ -138,12 +156,18 @@ bool make_cache_map(CUtensorMap* map, const attn_paged_kv_t* c, void* ptr, int b
                               static_cast<cuuint64_t>(c->page_size), static_cast<cuuint64_t>(c->n_pages)};
   const cuuint64_t strides[3] = {bytes(c->head_stride, c->H_kv), bytes(c->token_stride, c->page_size),
                                  bytes(c->page_stride, c->n_pages)};
+  // What L2 fetches at a time: no more than the bytes that lie together.  With 256 bytes, the 128-byte rows of an
+  // e4m3 cache [pages, slots, heads, 128] brought in the next head's row too: 393 MB of DRAM reads for 268.
+  const long long together = c->page_size > 1 && c->token_stride == c->D ? 256 : c->D * eb;
+  const CUtensorMapL2promotion promotion = together >= 256   ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B
+                                           : together >= 128 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B
+                                                             : CU_TENSOR_MAP_L2_PROMOTION_L2_64B;
   const cuuint32_t across = static_cast<cuuint32_t>(c->e4m3 ? c->D : 64);
   const cuuint32_t box[4] = {across, 1, static_cast<cuuint32_t>(box_rows), 1};
   const cuuint32_t estride[4] = {1, 1, 1, 1};
   return enc(map, c->e4m3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, ptr, dims, strides, box,
              estride, CU_TENSOR_MAP_INTERLEAVE_NONE,
-             across * eb == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             across * eb == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B, promotion,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -177,21 +201,6 @@ PagedWorkspace paged_workspace(int unit_rows, int D) {
   return w;
 }
 
-// Joins the cut units: a programmatic dependent, so that its launch overlaps the attention's tail.
-template <int D, int TILE_ROWS>
-cudaError_t launch_merge(const PagedParams& p, cudaStream_t s) {
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(kPagedCtas - 1, static_cast<unsigned>((p.unit_rows + 7) / 8));
-  cfg.blockDim = dim3(256);
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, paged_merge_kernel<D, TILE_ROWS>, p);
-}
-
 // Lays the workspace out, encodes the maps and launches `kern` (one CTA per SM), then the merge.
 template <int D, bool KV8, int TILE_ROWS, typename L>
 cudaError_t launch_paged(void (*kern)(CUtensorMap, CUtensorMap, CUtensorMap, PagedParams), const attn_paged_kv_t* c,
@@ -210,9 +219,10 @@ cudaError_t launch_paged(void (*kern)(CUtensorMap, CUtensorMap, CUtensorMap, Pag
   if (!make_cache_map(&mk, c, c->k, p.box_rows) || !make_cache_map(&mv, c, c->v, p.box_rows)) return cudaErrorUnknown;
   cudaError_t e = api_smem_opt_in(reinterpret_cast<const void*>(kern), L::SMEM_BYTES, seen);
   if (e != cudaSuccess) return e;
-  kern<<<kPagedCtas, L::THREADS, L::SMEM_BYTES, s>>>(mq, mk, mv, p);
-  e = cudaGetLastError();
-  return e != cudaSuccess ? e : launch_merge<D, TILE_ROWS>(p, s);
+  e = launch_dependent(kern, dim3(kPagedCtas), L::THREADS, L::SMEM_BYTES, s, mq, mk, mv, p);
+  if (e != cudaSuccess) return e;
+  return launch_dependent(paged_merge_kernel<D, TILE_ROWS>, dim3(kPagedCtas - 1, static_cast<unsigned>((p.unit_rows + 7) / 8)),
+                          256, 0, s, p);
 }
 
 // The kernel by the rows that a sequence's new tokens make in a kv group (max_new, or the mean where it is not

@@ -202,6 +202,13 @@ __global__ void __launch_bounds__(ChunkLayout<D, KV8>::THREADS, 1)
     tma_prefetch_desc(&tm_k);
     tma_prefetch_desc(&tm_v);
   }
+  PagedWalk walk;
+  if (warp == L::WARP_SCHED) {
+    // the CTA's stretch, while the others set up; a programmatic dependent of the kernel before it: nothing that
+    // kernel may have written is read before this wait, and the other roles start on what this warp publishes
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    paged_walk_start(p, walk, cta, static_cast<int>(gridDim.x), lane);
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -462,11 +469,9 @@ __global__ void __launch_bounds__(ChunkLayout<D, KV8>::THREADS, 1)
     }
   } else if (warp == L::WARP_SCHED) {
     // ===================== scheduler =====================
-    PagedWalk k;
-    paged_walk_start(p, k, cta, static_cast<int>(gridDim.x), lane);
-    if (lane == 0) p.cut[cta] = paged_cut(p, k, cta);
+    if (lane == 0) p.cut[cta] = paged_cut(p, walk, cta);
     for (int u = 0;; ++u) {
-      const PagedItem it = paged_walk_next(p, k, cta);
+      const PagedItem it = paged_walk_next(p, walk, cta);
       if (u >= L::NI && !__all_sync(0xffffffffu, mbar_wait(item_done(u), ((u / L::NI) - 1) & 1, ctl))) break;
       if (lane == 0) {
         volatile int* dst = reinterpret_cast<volatile int*>(sptr + L::ITEM_OFF + (u % L::NI) * sizeof(PagedItem));

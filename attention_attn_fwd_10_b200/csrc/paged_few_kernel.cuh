@@ -7,16 +7,22 @@
 // with K and V as the 128-row A operands straight from the pages and the few rows as B (N = NQ).
 // A softmax thread owns a key: it has NQ scores to exponentiate instead of 128, so the
 // chain of a block is a few hundred clocks and the kernel runs at the rate of its loads.
-// The running maximum of a column runs across threads; it is needed only where a score exceeds the one in use
-// by more than 2^TAU, which one barrier with an OR over the warpgroup tells.  Row sums stay per
+// The running maximum of a column runs across threads; it moves only where a weight would exceed
+// 2^(SHIFT + TAU) = 2^8, which one barrier with an OR over the warpgroup tells.  Row sums stay per
 // thread until the piece ends.  Warps:
 //   0-3, 4-7  softmax of the even and the odd blocks (two streams with statistics and
 //             accumulator of their own, joined at the piece's end by the first)
-//   8         TMA producer of Q (bf16 cache) and K
-//   9         tensor memory, MMA issue: S runs up to three blocks ahead of P V, across pieces
-//   10        TMA producer of V (zeros past a sequence's end)
+//   8         TMA producer of Q (bf16 cache), K and V
+//   9         tensor memory; issues the S MMAs, up to four blocks ahead of P V, across pieces
+//   10        issues the P V MMAs (and writes zeros over V's rows past a sequence's end)
 //   11        scheduler; e4m3 cache: also writes Q as two e4m3 terms
 // P^T goes to shared memory (the B operand's place), four buffers in turn.
+//
+// An MMA of M = 128 and N <= 32 takes 46 clk whatever N is (65 at N = 128), and issuing one about as long: with
+// one issuing thread for both products a block took 1800 clk.  e4m3 cache: q and the weights are sums of two
+// e4m3 terms (as in the chunk kernel), which stand side by side as 2 NQ columns of the same MMAs --
+// half the MMAs of two passes -- and are added in the softmax and in the epilogue.  The low terms carry a factor
+// of 16, so a weight's floor is 2^-14: with a row's largest weight at 2^SHIFT or more, 2^-17 of it.
 #pragma once
 
 #include "paged_plan.cuh"
@@ -36,6 +42,7 @@ struct FewLayout {
   static constexpr int Q_BYTES = (KV8 ? 2 : NBOX) * Q_COL;
   static constexpr int P_BYTES = 2 * NQ * 128;               // bf16: two 64-key columns; e4m3: the hi and the lo terms
   static constexpr int NBUF = 4;                             // score and P buffers in turn
+  static constexpr int NS = KV8 ? 2 * NQ : NQ;               // MMA columns: e4m3: the hi terms, then the lo terms
   // as many tiles as shared memory holds
   static constexpr int ROOM = 227 * 1024 - 1024 - 2 * Q_BYTES - NBUF * P_BYTES - 6 * 1024;
   static constexpr int ST = ROOM / (2 * KV_BYTES) < 8 ? ROOM / (2 * KV_BYTES) : 8;
@@ -51,8 +58,7 @@ struct FewLayout {
   static constexpr int B_K_EMPTY = B_K_FULL + ST;
   static constexpr int B_V_FULL = B_K_EMPTY + ST;
   static constexpr int B_V_EMPTY = B_V_FULL + ST;
-  static constexpr int B_V_RAW = B_V_EMPTY + ST;
-  static constexpr int B_S_FULL = B_V_RAW + 1;          // [NBUF]
+  static constexpr int B_S_FULL = B_V_EMPTY + ST;       // [NBUF]
   static constexpr int B_P_FULL = B_S_FULL + NBUF;      // [NBUF] four warps
   static constexpr int B_PV_DONE = B_P_FULL + NBUF;     // [NBUF]
   static constexpr int B_O_FINAL = B_PV_DONE + NBUF;
@@ -61,13 +67,14 @@ struct FewLayout {
   static constexpr int B_ITEM_FULL = B_XCHG_READ + 1;   // [NI]
   static constexpr int B_ITEM_EMPTY = B_ITEM_FULL + NI;
   static constexpr int B_DRAIN = B_ITEM_EMPTY + NI;
-  static constexpr int N_BARS = B_DRAIN + 1;
-  static constexpr int ITEM_READERS = 11;
+  static constexpr int N_BARS = B_DRAIN + 2;
+  static constexpr int ITEM_READERS = 11;  // 8 softmax warps, the producer, the two issuers
   static constexpr int ITEM_OFF = BAR_OFF + (8 * N_BARS + 15) / 16 * 16;
   static constexpr int CQ_OFF = ITEM_OFF + NI * static_cast<int>(sizeof(PagedItem));  // [NI][NQ] factors of the scores
   static constexpr int STAT_OFF = CQ_OFF + NI * NQ * 4;    // [2 streams][5][NQ]: four warps' sums, the maximum
   static constexpr int WMAX_OFF = STAT_OFF + 2 * 5 * NQ * 4;  // [2 streams][NQ][4 warps]
-  static constexpr int FAC_OFF = WMAX_OFF + 2 * NQ * 4 * 4;   // [2][NQ] factors of the accumulators
+  static constexpr int MOVED_OFF = WMAX_OFF + 2 * NQ * 4 * 4; // [2 streams][2][NQ]: the maxima in use, the last factors
+  static constexpr int FAC_OFF = MOVED_OFF + 2 * 2 * NQ * 4;  // [2][NQ] factors of the accumulators
   static constexpr int POS_OFF = FAC_OFF + 2 * NQ * 4;        // [NQ] position of a column
   static constexpr int TMEM_SLOT_OFF = POS_OFF + NQ * 4;
   static constexpr int ABORT_OFF = TMEM_SLOT_OFF + 4;
@@ -75,40 +82,52 @@ struct FewLayout {
   static constexpr int SMEM_BYTES = (SMEM_USED + 1024) > 122880 ? (SMEM_USED + 1024) : 122880;  // one CTA per SM
   static_assert(SMEM_BYTES <= 232448, "shared memory budget");
   static_assert(Q_COL % 1024 == 0 && P_BYTES % 2048 == 0, "operand tiles on swizzle boundaries");
-  __device__ static constexpr uint32_t s_col(int b) { return static_cast<uint32_t>(b) * NQ; }
-  __device__ static constexpr uint32_t o_col(int t) { return static_cast<uint32_t>(NBUF + t) * NQ; }
-  static constexpr uint32_t TMEM_COLS = NQ == 16 ? 128 : 256;
+  __device__ static constexpr uint32_t s_col(int b) { return static_cast<uint32_t>(b) * NS; }
+  __device__ static constexpr uint32_t o_col(int t) { return static_cast<uint32_t>(NBUF + t) * NS; }
+  static constexpr uint32_t TMEM_COLS = NS == 16 ? 128 : (NS == 32 ? 256 : 512);
   static constexpr int THREADS = 384;
-  static constexpr int WARP_K = 8, WARP_MMA = 9, WARP_V = 10, WARP_SCHED = 11;
-  static constexpr float SHIFT = KV8 ? 7.f : 0.f;  // as in the chunk kernel
-  static constexpr float TAU = KV8 ? 1.f : 8.f;
+  static constexpr int WARP_LOAD = 8, WARP_S = 9, WARP_PV = 10, WARP_SCHED = 11;
+  // weights up to 2^(SHIFT + TAU) = 2^8; a column's largest at 2^SHIFT or more
+  static constexpr float SHIFT = KV8 ? 3.f : 0.f;
+  static constexpr float TAU = KV8 ? 5.f : 8.f;
+  static constexpr float LO = 1.f / 16.f;  // e4m3: what a lo term stands for
   static constexpr uint32_t HI = ROW_BYTES == 128 ? sdesc_sw128_hi(1024) : sdesc_sw64_hi(512);
   static constexpr uint32_t HI128 = sdesc_sw128_hi(1024);
 };
 
-constexpr float kNoKeyYet = -1e30f;  // a column's maximum before its first key
+constexpr float kNoKeyYet = -3e38f;  // a column's maximum before its first key
 
 template <int N>
 __device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, uint32_t* r) {
-  static_assert(N == 16 || N == 32, "columns");
-  if constexpr (N == 16)
+  static_assert(N == 16 || N == 32 || N == 64, "columns");
+  if constexpr (N == 16) {
     tmem_ld16(taddr, r);
-  else
-    tmem_ld32(taddr, r);
-}
-template <int N>
-__device__ __forceinline__ void tmem_ld_cols_wait(uint32_t* r) {
-  if constexpr (N == 16)
     tmem_ld_wait16(r);
-  else
+  } else if constexpr (N == 32) {
+    tmem_ld32(taddr, r);
     tmem_ld_wait(r);
+  } else {
+    tmem_ld32(taddr, r);
+    tmem_ld32(taddr + 32, r + 32);
+    tmem_ld_wait(r);
+    tmem_ld_wait(r + 32);
+  }
 }
-template <int N>
-__device__ __forceinline__ void tmem_st_cols(uint32_t taddr, const uint32_t* r) {
-  if constexpr (N == 16)
-    tmem_st16(taddr, r);
-  else
-    tmem_st32(taddr, r);
+// Multiplies a 32-lane accumulator's columns by per-column factors (e4m3: both terms' columns).
+template <int NQ, int NS>
+__device__ __forceinline__ void tmem_scale_cols(uint32_t taddr, const float* alpha) {
+#pragma unroll
+  for (int x = 0; x < NS; x += NQ) {
+    uint32_t r[NQ];
+    tmem_ld_cols<NQ>(taddr + x, r);
+#pragma unroll
+    for (int q = 0; q < NQ; ++q) r[q] = __float_as_uint(__uint_as_float(r[q]) * alpha[q]);
+    if constexpr (NQ == 16)
+      tmem_st16(taddr + x, r);
+    else
+      tmem_st32(taddr + x, r);
+  }
+  tmem_st_wait();
 }
 
 // Barrier of one warpgroup (id 1 or 2), and the same with the OR of a predicate.
@@ -126,16 +145,24 @@ __device__ __forceinline__ bool group_any(int id, bool x) {
   return r != 0;
 }
 
-__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(bar), "r"(parity)
-      : "memory");
-  return ok != 0;
+// One value per column from a warp's 32 x N values: lane q (and q + 16 for N = 16) gets column q's reduction,
+// by halving exchanges: each step a lane keeps the half of its columns that its own number names.
+template <int N, typename Op>
+__device__ __forceinline__ float warp_columns(const float* x, int lane, Op op) {
+  float v[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) v[i] = x[i];
+#pragma unroll
+  for (int half = N / 2; half > 0; half /= 2) {
+    const bool up = (lane & half) != 0;
+#pragma unroll
+    for (int i = 0; i < half; ++i) {
+      const float other = __shfl_xor_sync(0xffffffffu, up ? v[i] : v[i + half], half);
+      v[i] = op(up ? v[i + half] : v[i], other);
+    }
+  }
+  if (N == 16) v[0] = op(v[0], __shfl_xor_sync(0xffffffffu, v[0], 16));
+  return v[0];
 }
 
 template <int D, bool KV8, int NQ>
@@ -166,19 +193,25 @@ __global__ void __launch_bounds__(FewLayout<D, KV8, NQ>::THREADS, 1)
     *abort_flag = 0;
     fence_mbar_init();
   }
-  if (warp == L::WARP_MMA) {
+  if (warp == L::WARP_S) {
     tmem_alloc(sbase + L::TMEM_SLOT_OFF, L::TMEM_COLS);
     tmem_relinquish();
   }
-  if (warp == L::WARP_K && lane == 0) {
+  if (warp == L::WARP_LOAD && lane == 0) {
     if (!KV8) tma_prefetch_desc(&tm_q);
     tma_prefetch_desc(&tm_k);
     tma_prefetch_desc(&tm_v);
   }
   // Q rows that no load reaches stay zero (padding columns of the products)
-  for (int i = threadIdx.x; i < 2 * L::Q_BYTES / 16; i += L::THREADS)
-    *reinterpret_cast<uint4*>(sptr + L::Q_OFF + i * 16) = make_uint4(0, 0, 0, 0);
+  for (int i = threadIdx.x; i < 2 * L::Q_BYTES / 16; i += 256)
+    if (warp < 8) *reinterpret_cast<uint4*>(sptr + L::Q_OFF + i * 16) = make_uint4(0, 0, 0, 0);
   if (threadIdx.x < NQ) reinterpret_cast<int*>(sptr + L::POS_OFF)[threadIdx.x] = static_cast<int>(threadIdx.x) / p.group;
+  PagedWalk walk;
+  if (warp == L::WARP_SCHED) {
+    // the CTA's stretch, while the others set up (as in the chunk kernel)
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    paged_walk_start(p, walk, cta, static_cast<int>(gridDim.x), lane);
+  }
   fence_proxy_async_smem();
   tc_fence_before();
   __syncthreads();
@@ -191,8 +224,8 @@ __global__ void __launch_bounds__(FewLayout<D, KV8, NQ>::THREADS, 1)
   auto wait_item = [&](int u) { return mbar_wait(bar(L::B_ITEM_FULL + u % L::NI), (u / L::NI) & 1, ctl); };
   auto item_done = [&](int u) { return bar(L::B_ITEM_EMPTY + u % L::NI); };
 
-  if (warp == L::WARP_K) {
-    // ===================== TMA producer: Q, K =====================
+  if (warp == L::WARP_LOAD) {
+    // ===================== TMA producer: Q, K, V =====================
     int kn = 0, qn = 0;
     bool ok = true;
     for (int u = 0; ok; ++u) {
@@ -215,13 +248,18 @@ __global__ void __launch_bounds__(FewLayout<D, KV8, NQ>::THREADS, 1)
         ++qn;
       }
       PageWindow win{-1, -1};
-      for (int j = 0; ok && j < n_loads; ++j) {
+      for (int j = 0; ok && j < n_loads; ++j, ++kn) {
         const int s = kn % L::ST;
-        if (kn >= L::ST && !(ok = __all_sync(0xffffffffu, mbar_wait(bar(L::B_K_EMPTY + s), ((kn / L::ST) - 1) & 1, ctl))))
-          break;
+        const uint32_t ph = ((kn / L::ST) - 1) & 1;
+        if (kn >= L::ST && !(ok = __all_sync(0xffffffffu, mbar_wait(bar(L::B_K_EMPTY + s), ph, ctl)))) break;
         load_block<L::NBOX, L::ROW_BYTES>(p, &tm_k, sbase + L::K_OFF + s * L::KV_BYTES, bar(L::B_K_FULL + s), win, seq, head,
                                           len, j0 + j, lane);
-        ++kn;
+        if (kn >= L::ST && !(ok = __all_sync(0xffffffffu, mbar_wait(bar(L::B_V_EMPTY + s), ph, ctl)))) {
+          mbar_wait_drain(bar(L::B_K_FULL + s), (kn / L::ST) & 1, 1000000000ull);  // its V was not asked for
+          break;
+        }
+        load_block<L::NBOX, L::ROW_BYTES>(p, &tm_v, sbase + L::V_OFF + s * L::KV_BYTES, bar(L::B_V_FULL + s), win, seq, head,
+                                          len, j0 + j, lane);
       }
     }
     // Drain: every load this warp issued has landed before the CTA may exit.
@@ -230,182 +268,130 @@ __global__ void __launch_bounds__(FewLayout<D, KV8, NQ>::THREADS, 1)
     for (int i = 0; i < L::ST && i < kn; ++i) {
       const int n = kn - 1 - i;
       mbar_wait_drain(bar(L::B_K_FULL + n % L::ST), (n / L::ST) & 1, 1000000000ull);
-    }
-  } else if (warp == L::WARP_V) {
-    // ===================== TMA producer: V =====================
-    int vn = 0, raw_n = 0;
-    bool ok = true;
-    for (int u = 0; ok; ++u) {
-      if (!(ok = __all_sync(0xffffffffu, wait_item(u)))) break;
-      const volatile PagedItem* it = item_at(u);
-      const int row0 = it->row0, head = it->head, seq = it->seq, len = it->len, j0 = it->j0, n_loads = it->n_loads;
-      mbar_arrive_warp(item_done(u));
-      if (row0 < 0) break;
-      PageWindow win{-1, -1};
-      for (int j = 0; ok && j < n_loads; ++j) {
-        const int s = vn % L::ST;
-        if (vn >= L::ST && !(ok = __all_sync(0xffffffffu, mbar_wait(bar(L::B_V_EMPTY + s), ((vn / L::ST) - 1) & 1, ctl))))
-          break;
-        const uint32_t dst = sbase + L::V_OFF + s * L::KV_BYTES;
-        const int live = len - (j0 + j) * L::BN;  // keys of the block that the sequence has
-        if (live >= L::BN) {
-          load_block<L::NBOX, L::ROW_BYTES>(p, &tm_v, dst, bar(L::B_V_FULL + s), win, seq, head, len, j0 + j, lane);
-          ++vn;
-        } else {
-          load_block<L::NBOX, L::ROW_BYTES>(p, &tm_v, dst, bar(L::B_V_RAW), win, seq, head, len, j0 + j, lane);
-          ok = __all_sync(0xffffffffu, mbar_wait(bar(L::B_V_RAW), raw_n & 1, ctl));
-          if (ok) {
-            zero_tail<L::NBOX, L::ROW_BYTES>(sptr + L::V_OFF + s * L::KV_BYTES, live, lane);
-            if (lane == 0) mbar_arrive(bar(L::B_V_FULL + s));
-            ++vn;
-          } else {
-            mbar_wait_drain(bar(L::B_V_RAW), raw_n & 1, 1000000000ull);
-          }
-          ++raw_n;
-        }
-      }
-    }
-    for (int i = 0; i < L::ST && i < vn; ++i) {
-      const int n = vn - 1 - i;
       mbar_wait_drain(bar(L::B_V_FULL + n % L::ST), (n / L::ST) & 1, 1000000000ull);
     }
-  } else if (warp == L::WARP_MMA) {
-    // ===================== MMA issuer =====================
+  } else if (warp == L::WARP_S) {
+    // ===================== S^T = K Q^T =====================
     if (lane == 0) {
-      constexpr uint32_t IDESC_S = KV8 ? idesc_e4m3_f32(128, NQ) : idesc_bf16_f32(128, NQ, false, false);
-      constexpr uint32_t IDESC_PV = KV8 ? (idesc_e4m3_f32(D, NQ) | (1u << 15)) : idesc_bf16_f32(D, NQ, true, false);
-      auto issue_s = [&](int buf, int qs, int stage) {
-        const uint32_t kd = sdesc_lo(sbase + L::K_OFF + stage * L::KV_BYTES, 16);
-        const uint32_t qd = sdesc_lo(sbase + L::Q_OFF + qs * L::Q_BYTES, 16);
-        if constexpr (KV8) {
-#pragma unroll
-          for (int kk = 0; kk < 2 * (D / 32); ++kk) {  // q's hi terms, then the lo terms
-            const uint32_t off = (kk % (D / 32)) * 32;
-            umma_ss_f8_h(tmem + L::s_col(buf), kd + (off >> 4), L::HI, qd + ((kk / (D / 32)) * L::Q_COL + off >> 4), L::HI,
-                         IDESC_S, kk > 0 ? 1u : 0u);
-          }
-        } else {
-#pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk) {
-            const uint32_t off = (kk & 3) * 32;
-            umma_ss_h(tmem + L::s_col(buf), kd + ((kk >> 2) * L::BOX_BYTES + off >> 4), L::HI,
-                      qd + ((kk >> 2) * L::Q_COL + off >> 4), L::HI, IDESC_S, kk > 0 ? 1u : 0u);
-          }
-        }
-        umma_commit(bar(L::B_S_FULL + buf));
-      };
-      auto issue_pv = [&](int t, int buf, int stage, bool acc) {
-        const uint32_t pd = sdesc_lo(sbase + L::P_OFF + buf * L::P_BYTES, 16);
-        if constexpr (KV8) {
-          const uint32_t vd = sdesc_lo(sbase + L::V_OFF + stage * L::KV_BYTES, 16);
-#pragma unroll
-          for (int kk = 0; kk < 8; ++kk)  // 32 keys each: the hi terms, then the lo terms
-            umma_ss_f8_h(tmem + L::o_col(t), vd + ((kk & 3) * 32 * L::ROW_BYTES >> 4), L::HI,
-                         pd + ((kk >> 2) * NQ * 128 + (kk & 3) * 32 >> 4), L::HI128, IDESC_PV, (acc || kk > 0) ? 1u : 0u);
-        } else {
-          const uint32_t vd = sdesc_lo(sbase + L::V_OFF + stage * L::KV_BYTES, L::BOX_BYTES);
-#pragma unroll
-          for (int kk = 0; kk < 8; ++kk)  // 16 keys each
-            umma_ss_h(tmem + L::o_col(t), vd + (kk * 2048 >> 4), L::HI,
-                      pd + ((kk >> 2) * NQ * 128 + (kk & 3) * 32 >> 4), L::HI128, IDESC_PV, (acc || kk > 0) ? 1u : 0u);
-        }
-        umma_commit(bar(L::B_PV_DONE + buf));
-      };
-      // Two cursors over the CTA's blocks, in order: S of block gs, P V of block gp <= gs.  Scores may run NBUF blocks
-      // ahead at most: buffer gs % NBUF was read before P(gs - NBUF) was published.  Whichever is ready goes first.
-      int gs = 0, gp = 0;
-      int u = 0, left = 0, qi = 0;   // the S cursor's piece: number, blocks left, Q tile
-      int g0 = 0;                    // its first block
-      bool have = false, ended = false, fresh = false;
-      uint32_t flags = 0;            // of block g, four bits at 4 (g % NBUF): 1 = first of its stream, 2 = last of its piece
-      uint64_t t0 = 0;
-      uint32_t spins = 0;
-      while (!ended || gp < gs) {
-        bool did = false;
-        if (!ended && !have && mbar_test(bar(L::B_ITEM_FULL + u % L::NI), (u / L::NI) & 1)) {
-          const volatile PagedItem* it = item_at(u);
-          ended = it->row0 < 0;
-          left = it->n_loads;
-          mbar_arrive(item_done(u));
-          ++u;
-          have = !ended && left > 0;
-          fresh = have;
-          g0 = gs;
-          did = true;
-        }
-        if (have && gs - gp < L::NBUF && mbar_test(bar(L::B_K_FULL + gs % L::ST), (gs / L::ST) & 1) &&
-            (!fresh || mbar_test(bar(L::B_Q_FULL + (qi & 1)), (qi >> 1) & 1))) {
-          fresh = false;
+      constexpr uint32_t IDESC = KV8 ? idesc_e4m3_f32(128, L::NS) : idesc_bf16_f32(128, L::NS, false, false);
+      int g = 0, qi = 0;
+      bool ok = true;
+      for (int u = 0; ok; ++u) {
+        if (!(ok = wait_item(u))) break;
+        const volatile PagedItem* it = item_at(u);
+        const int row0 = it->row0, n = it->n_loads;
+        mbar_arrive(item_done(u));
+        if (row0 < 0) break;
+        for (int j = 0; j < n; ++j, ++g) {
+          const int buf = g % L::NBUF, stage = g % L::ST;
+          ok = mbar_wait(bar(L::B_K_FULL + stage), (g / L::ST) & 1, ctl);
+          // four blocks ago: the scores were read before P was published, and P V is complete, so the softmax
+          // that S_FULL wakes finds its P buffer free
+          if (ok && g >= L::NBUF) ok = mbar_wait(bar(L::B_PV_DONE + buf), ((g / L::NBUF) - 1) & 1, ctl);
+          if (ok && j == 0) ok = mbar_wait(bar(L::B_Q_FULL + (qi & 1)), (qi >> 1) & 1, ctl);
+          if (!ok) break;
           tc_fence_after();
-          const int buf = gs % L::NBUF;
-          issue_s(buf, qi & 1, gs % L::ST);
-          umma_commit(bar(L::B_K_EMPTY + gs % L::ST));
-          --left;
-          flags = (flags & ~(0xfu << (4 * buf))) | (((gs - g0 < 2 ? 1u : 0u) | (left == 0 ? 2u : 0u)) << (4 * buf));
-          ++gs;
-          if (left == 0) {
+          const uint32_t kd = sdesc_lo(sbase + L::K_OFF + stage * L::KV_BYTES, 16);
+          const uint32_t qd = sdesc_lo(sbase + L::Q_OFF + (qi & 1) * L::Q_BYTES, 16);
+          if constexpr (KV8) {
+#pragma unroll
+            for (int kk = 0; kk < D / 32; ++kk)
+              umma_ss_f8_h(tmem + L::s_col(buf), kd + (kk * 32 >> 4), L::HI, qd + (kk * 32 >> 4), L::HI, IDESC, kk > 0 ? 1u : 0u);
+          } else {
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk) {
+              const uint32_t off = (kk & 3) * 32;
+              umma_ss_h(tmem + L::s_col(buf), kd + ((kk >> 2) * L::BOX_BYTES + off >> 4), L::HI,
+                        qd + ((kk >> 2) * L::Q_COL + off >> 4), L::HI, IDESC, kk > 0 ? 1u : 0u);
+            }
+          }
+          umma_commit(bar(L::B_S_FULL + buf));
+          umma_commit(bar(L::B_K_EMPTY + stage));
+          if (j == n - 1) {
             umma_commit(bar(L::B_Q_EMPTY + (qi & 1)));
             ++qi;
-            have = false;
-          }
-          did = true;
-        }
-        if (gp < gs) {
-          const int buf = gp % L::NBUF;
-          if (mbar_test(bar(L::B_P_FULL + buf), (gp / L::NBUF) & 1) && mbar_test(bar(L::B_V_FULL + gp % L::ST), (gp / L::ST) & 1)) {
-            tc_fence_after();
-            const uint32_t f = flags >> (4 * buf);
-            issue_pv(gp & 1, buf, gp % L::ST, (f & 1u) == 0);
-            umma_commit(bar(L::B_V_EMPTY + gp % L::ST));
-            if (f & 2u) umma_commit(bar(L::B_O_FINAL));
-            ++gp;
-            did = true;
-          }
-        }
-        if (did) {
-          spins = 0;
-        } else if ((++spins & 63u) == 0) {  // the wait's bound, as in mbar_wait
-          if (*abort_flag) break;
-          const uint64_t now = globaltimer_ns();
-          if (spins == 64) t0 = now;
-          if (now - t0 > p.wait_limit_ns) {
-            *abort_flag = 1;
-            atomicExch(p.status, kDevWaitTimeout);
-            break;
           }
         }
       }
       umma_commit(bar(L::B_DRAIN));  // no MMA may still write tensor memory when it is released
       mbar_wait_drain(bar(L::B_DRAIN), 0, 1000000000ull);
     }
+  } else if (warp == L::WARP_PV) {
+    // ===================== O^T += V^T P^T =====================
+    constexpr uint32_t IDESC = KV8 ? (idesc_e4m3_f32(D, L::NS) | (1u << 15)) : idesc_bf16_f32(D, L::NS, true, false);
+    int g = 0;
+    bool ok = true;
+    for (int u = 0; ok; ++u) {
+      if (!(ok = __all_sync(0xffffffffu, wait_item(u)))) break;
+      const volatile PagedItem* it = item_at(u);
+      const int row0 = it->row0, n = it->n_loads, len = it->len, j0 = it->j0;
+      mbar_arrive_warp(item_done(u));
+      if (row0 < 0) break;
+      for (int j = 0; j < n; ++j, ++g) {
+        const int buf = g % L::NBUF, stage = g % L::ST;
+        ok = mbar_wait(bar(L::B_V_FULL + stage), (g / L::ST) & 1, ctl);
+        if (!(ok = __all_sync(0xffffffffu, ok))) break;
+        const int live = len - (j0 + j) * L::BN;  // keys of the block that the sequence has
+        if (live < L::BN) zero_tail<L::NBOX, L::ROW_BYTES>(sptr + L::V_OFF + stage * L::KV_BYTES, live, lane);
+        ok = mbar_wait(bar(L::B_P_FULL + buf), (g / L::NBUF) & 1, ctl);
+        if (!(ok = __all_sync(0xffffffffu, ok))) break;
+        if (lane == 0) {
+          tc_fence_after();
+          const uint32_t od = tmem + L::o_col(g & 1);
+          const uint32_t pd = sdesc_lo(sbase + L::P_OFF + buf * L::P_BYTES, 16);
+          if constexpr (KV8) {
+            const uint32_t vd = sdesc_lo(sbase + L::V_OFF + stage * L::KV_BYTES, 16);
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)  // 32 keys each
+              umma_ss_f8_h(od, vd + (kk * 32 * L::ROW_BYTES >> 4), L::HI, pd + (kk * 32 >> 4), L::HI128, IDESC,
+                           (j > 1 || kk > 0) ? 1u : 0u);
+          } else {
+            const uint32_t vd = sdesc_lo(sbase + L::V_OFF + stage * L::KV_BYTES, L::BOX_BYTES);
+#pragma unroll
+            for (int kk = 0; kk < 8; ++kk)  // 16 keys each
+              umma_ss_h(od, vd + (kk * 2048 >> 4), L::HI, pd + ((kk >> 2) * NQ * 128 + (kk & 3) * 32 >> 4), L::HI128, IDESC,
+                        (j > 1 || kk > 0) ? 1u : 0u);
+          }
+          umma_commit(bar(L::B_PV_DONE + buf));
+          umma_commit(bar(L::B_V_EMPTY + stage));
+          if (j == n - 1) umma_commit(bar(L::B_O_FINAL));
+        }
+        __syncwarp();
+      }
+    }
+    if (lane == 0) {
+      umma_commit(bar(L::B_DRAIN + 1));
+      mbar_wait_drain(bar(L::B_DRAIN + 1), 0, 1000000000ull);
+    }
   } else if (warp == L::WARP_SCHED) {
     // ===================== scheduler =====================
-    PagedWalk k;
-    paged_walk_start(p, k, cta, static_cast<int>(gridDim.x), lane);
-    if (lane == 0) p.cut[cta] = paged_cut(p, k, cta);
+    if (lane == 0) p.cut[cta] = paged_cut(p, walk, cta);
     int qn = 0;
     for (int u = 0;; ++u) {
-      const PagedItem it = paged_walk_next(p, k, cta);
+      const PagedItem it = paged_walk_next(p, walk, cta);
       if (u >= L::NI && !__all_sync(0xffffffffu, mbar_wait(item_done(u), ((u / L::NI) - 1) & 1, ctl))) break;
       const bool q_here = KV8 && it.row0 >= 0 && it.n_loads > 0;
       const bool real = lane < p.group * it.n_pos;  // lane = column of the unit
-      const uint4* src = nullptr;
+      uint4 w[KV8 ? D / 8 : 1];
       uint32_t up = 0;
       if (q_here) {
         // the power of two that puts the row's largest element into [128, 256)
+#pragma unroll
+        for (int i = 0; i < (KV8 ? D / 8 : 1); ++i) w[i] = make_uint4(0, 0, 0, 0);
         if (real) {
           const int pos = lane / p.group;
-          src = reinterpret_cast<const uint4*>(p.q + (static_cast<long long>(it.row0) + pos) * p.q_stride +
-                                               static_cast<long long>(it.head * p.group + lane - pos * p.group) * D);
-          uint32_t most = 0;
-#pragma unroll 4
-          for (int i = 0; i < D / 8; ++i) {
-            const uint4 w = src[i];
-            most = max(max(most, max(max(w.x & 0x7f80u, w.y & 0x7f80u), max(w.z & 0x7f80u, w.w & 0x7f80u))),
-                       max(max((w.x >> 16) & 0x7f80u, (w.y >> 16) & 0x7f80u), max((w.z >> 16) & 0x7f80u, (w.w >> 16) & 0x7f80u)));
-          }
-          up = q_power(most);
+          const uint4* src = reinterpret_cast<const uint4*>(p.q + (static_cast<long long>(it.row0) + pos) * p.q_stride +
+                                                            static_cast<long long>(it.head * p.group + lane - pos * p.group) * D);
+#pragma unroll
+          for (int i = 0; i < (KV8 ? D / 8 : 1); ++i) w[i] = src[i];
         }
+        uint32_t most = 0;
+#pragma unroll
+        for (int i = 0; i < (KV8 ? D / 8 : 1); ++i)
+          most = max(max(most, max(max(w[i].x & 0x7f80u, w[i].y & 0x7f80u), max(w[i].z & 0x7f80u, w[i].w & 0x7f80u))),
+                     max(max((w[i].x >> 16) & 0x7f80u, (w[i].y >> 16) & 0x7f80u),
+                         max((w[i].z >> 16) & 0x7f80u, (w[i].w >> 16) & 0x7f80u)));
+        up = q_power(most);
         if (lane < NQ)
           reinterpret_cast<float*>(sptr + L::CQ_OFF)[(u % L::NI) * NQ + lane] =
               real ? q_factor(p.scale_log2, up) : 0.f;
@@ -426,22 +412,21 @@ __global__ void __launch_bounds__(FewLayout<D, KV8, NQ>::THREADS, 1)
           uint8_t* dst = sptr + L::Q_OFF + qs * L::Q_BYTES + lane * L::ROW_BYTES;
           const int sw = L::ROW_BYTES == 128 ? (lane & 7) : ((lane >> 1) & 3);
           const float scale = __uint_as_float(up << 23);
-#pragma unroll 1
-          for (int ch = 0; ch < D / 16; ++ch) {
-            uint32_t hi[4] = {0, 0, 0, 0}, lo[4] = {0, 0, 0, 0};
-            if (real) {
-              const uint4 w0 = src[2 * ch], w1 = src[2 * ch + 1];
-              const uint32_t x[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
 #pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                uint32_t h0, l0, h1, l1;
-                split_e4m3x2(bf_lo(x[2 * i]) * scale, bf_hi(x[2 * i]) * scale, h0, l0);
-                split_e4m3x2(bf_lo(x[2 * i + 1]) * scale, bf_hi(x[2 * i + 1]) * scale, h1, l1);
-                hi[i] = h0 | (h1 << 16);
-                lo[i] = l0 | (l1 << 16);
-              }
+          for (int ch = 0; ch < (KV8 ? D / 16 : 0); ++ch) {
+            uint32_t hi[4], lo[4];
+            const uint32_t x[8] = {w[2 * ch].x,     w[2 * ch].y,     w[2 * ch].z,     w[2 * ch].w,
+                                   w[2 * ch + 1].x, w[2 * ch + 1].y, w[2 * ch + 1].z, w[2 * ch + 1].w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              uint32_t h0, l0, h1, l1;
+              split16_e4m3x2(bf_lo(x[2 * i]) * scale, bf_hi(x[2 * i]) * scale, h0, l0);
+              split16_e4m3x2(bf_lo(x[2 * i + 1]) * scale, bf_hi(x[2 * i + 1]) * scale, h1, l1);
+              hi[i] = h0 | (h1 << 16);
+              lo[i] = l0 | (l1 << 16);
             }
             *reinterpret_cast<uint4*>(dst + ((ch ^ sw) * 16)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+            // (lo terms: 16 times the remainder)
             *reinterpret_cast<uint4*>(dst + L::Q_COL + ((ch ^ sw) * 16)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
           }
         }
@@ -458,6 +443,7 @@ __global__ void __launch_bounds__(FewLayout<D, KV8, NQ>::THREADS, 1)
     const uint32_t lane_addr = static_cast<uint32_t>(wq * 32) << 16;
     float* const stat = reinterpret_cast<float*>(sptr + L::STAT_OFF);
     float* const wmax = reinterpret_cast<float*>(sptr + L::WMAX_OFF) + t * NQ * 4;
+    float* const moved = reinterpret_cast<float*>(sptr + L::MOVED_OFF) + t * 2 * NQ;
     float* const fac = reinterpret_cast<float*>(sptr + L::FAC_OFF);
     const int* const pos_of = reinterpret_cast<const int*>(sptr + L::POS_OFF);
     // where this thread's key sits in a P row: bf16 64-key columns, e4m3 one 128-key column
@@ -489,10 +475,13 @@ __global__ void __launch_bounds__(FewLayout<D, KV8, NQ>::THREADS, 1)
         const int buf = gg % L::NBUF;
         wait_for(L::B_S_FULL + buf, gg / L::NBUF);
         tc_fence_after();
-        uint32_t sr[NQ];
-        tmem_ld_cols<NQ>(tmem + lane_addr + L::s_col(buf), sr);
-        tmem_ld_cols_wait<NQ>(sr);
+        uint32_t sr[L::NS];
+        tmem_ld_cols<L::NS>(tmem + lane_addr + L::s_col(buf), sr);
         float* s = reinterpret_cast<float*>(sr);
+        if constexpr (KV8) {
+#pragma unroll
+          for (int q = 0; q < NQ; ++q) s[q] = fmaf(s[NQ + q], L::LO, s[q]);
+        }
         // scores in base-2 units
         if constexpr (KV8) {
           const float4* cq = reinterpret_cast<const float4*>(sptr + L::CQ_OFF + (u % L::NI) * NQ * 4);
@@ -519,48 +508,39 @@ __global__ void __launch_bounds__(FewLayout<D, KV8, NQ>::THREADS, 1)
         float over = s[0] - m[0];
 #pragma unroll
         for (int q = 1; q < NQ; ++q) over = fmaxf(over, s[q] - m[q]);
-        if (group_any(1 + t, over > L::TAU || !ok)) {
+        if (group_any(1 + t, over > L::SHIFT + L::TAU || !ok)) {
           if ((failed = group_any(1 + t, !ok))) break;
-          // some column's maximum moves: the block's maxima, over the four warps
-          float mine = 0.f;
-#pragma unroll
-          for (int q = 0; q < NQ; ++q) {
-            float x = s[q];
-#pragma unroll
-            for (int off = 16; off > 0; off >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, off));
-            if (lane == q) mine = x;
-          }
+          // some column's maximum moves: the block's maxima over the four warps; thread q of the stream decides for
+          // column q
+          const float mine = warp_columns<NQ>(s, lane, [](float x, float y) { return fmaxf(x, y); });
           if (lane < NQ) wmax[lane * 4 + wq] = mine;
+          group_sync(1 + t);
+          if ((threadIdx.x & 127) < real) {
+            const int q = threadIdx.x & 127;
+            const float4 w = reinterpret_cast<const float4*>(wmax)[q];
+            const float top = fmaxf(fmaxf(w.x, w.y), fmaxf(w.z, w.w));
+            const float old = first ? kNoKeyYet : moved[q];
+            // (false for a column with no visible key yet: -inf)
+            const bool moves = top - old > L::SHIFT + L::TAU;
+            const float to = moves ? top - L::SHIFT : old;
+            moved[q] = to;
+            moved[NQ + q] = moves ? exp2_mufu(old - to) : 1.f;
+          }
           group_sync(1 + t);
           float alpha[NQ];
 #pragma unroll
           for (int q = 0; q < NQ; ++q) {
-            const float4 w = reinterpret_cast<const float4*>(wmax)[q];
-            const float top = fmaxf(fmaxf(w.x, w.y), fmaxf(w.z, w.w));
-            alpha[q] = 1.f;
-            if (top - m[q] > L::TAU) {  // (false for a column with no visible key: -inf)
-              const float to = top - L::SHIFT;
-              alpha[q] = exp2_mufu(m[q] - to);
-              m[q] = to;
-              l[q] *= alpha[q];
-            }
+            if (q < real) m[q] = moved[q];
+            alpha[q] = q < real ? moved[NQ + q] : 1.f;
+            l[q] *= alpha[q];
           }
           if (!first) {
             // the stream's earlier P V must be complete before its accumulator is scaled
             wait_for(L::B_PV_DONE + (gg - 2) % L::NBUF, (gg - 2) / L::NBUF);
             tc_fence_after();
-            uint32_t orr[NQ];
-            tmem_ld_cols<NQ>(tmem + lane_addr + L::o_col(t), orr);
-            tmem_ld_cols_wait<NQ>(orr);
-#pragma unroll
-            for (int q = 0; q < NQ; ++q) orr[q] = __float_as_uint(__uint_as_float(orr[q]) * alpha[q]);
-            tmem_st_cols<NQ>(tmem + lane_addr + L::o_col(t), orr);
-            tmem_st_wait();
+            tmem_scale_cols<NQ, L::NS>(tmem + lane_addr + L::o_col(t), alpha);
           }
-          group_sync(1 + t);  // wmax is read
         }
-        // P buffer free: the P V that read it four blocks ago is complete
-        if (gg >= L::NBUF) wait_for(L::B_PV_DONE + buf, gg / L::NBUF - 1);
         uint8_t* const pb = sptr + L::P_OFF + buf * L::P_BYTES + p_at;
 #pragma unroll
         for (int q = 0; q < NQ; q += 2) {
@@ -571,7 +551,7 @@ __global__ void __launch_bounds__(FewLayout<D, KV8, NQ>::THREADS, 1)
           uint8_t* const a1 = pb + (q + 1) * 128 + ((p_chunk ^ ((q + 1) & 7)) << 4);
           if constexpr (KV8) {
             uint32_t hi, lo;
-            split_e4m3x2(e0, e1, hi, lo);
+            split16_e4m3x2(e0, e1, hi, lo);
             a0[0] = static_cast<uint8_t>(hi);
             a1[0] = static_cast<uint8_t>(hi >> 8);
             a0[NQ * 128] = static_cast<uint8_t>(lo);
@@ -594,20 +574,10 @@ __global__ void __launch_bounds__(FewLayout<D, KV8, NQ>::THREADS, 1)
       if (nb > 0) {
         // stream 1 has no block in this piece: its accumulator is not rewritten, but its place in `stat` is
         if (first && t == 1 && items > 0) wait_for(L::B_XCHG_READ, items - 1);
-        float mine = 0.f, mm = 0.f;
-#pragma unroll
-        for (int q = 0; q < NQ; ++q) {
-          float x = l[q];
-#pragma unroll
-          for (int off = 16; off > 0; off >>= 1) x += __shfl_xor_sync(0xffffffffu, x, off);
-          if (lane == q) {
-            mine = x;
-            mm = m[q];
-          }
-        }
+        const float mine = warp_columns<NQ>(l, lane, [](float x, float y) { return x + y; });
         if (lane < NQ) {
           stat[(t * 5 + wq) * NQ + lane] = mine;
-          if (wq == 0) stat[(t * 5 + 4) * NQ + lane] = mm;
+          if (wq == 0) stat[(t * 5 + 4) * NQ + lane] = first ? kNoKeyYet : moved[lane];
         }
         if (t == 1) {
           mbar_arrive_warp(bar(L::B_XCHG));
@@ -649,38 +619,47 @@ __global__ void __launch_bounds__(FewLayout<D, KV8, NQ>::THREADS, 1)
           }
         }
         group_sync(1);
-        uint32_t oa[NQ], ob[NQ];
         // a stream without blocks in the piece has no accumulator (fac 0, not read)
         const bool have_a = nb > 1 || (nb == 1 && (g & 1) == 0), have_b = nb > 1 || (nb == 1 && (g & 1) == 1);
-#pragma unroll
-        for (int q = 0; q < NQ; ++q) oa[q] = ob[q] = 0u;
         if (nb > 0) {
           wait_for(L::B_O_FINAL, items);
           tc_fence_after();
-          if (have_a) tmem_ld_cols<NQ>(tmem + lane_addr + L::o_col(0), oa);
-          if (have_b) tmem_ld_cols<NQ>(tmem + lane_addr + L::o_col(1), ob);
-          if (have_a) tmem_ld_cols_wait<NQ>(oa);
-          if (have_b) tmem_ld_cols_wait<NQ>(ob);
         }
-        // stat and the accumulators are read (fac is this stream's own)
-        tc_fence_before();
-        if (nb > 0) mbar_arrive_warp(bar(L::B_XCHG_READ));
         // row d of O^T: TMEM lane d, or lanes 32 g .. 32 g + 15 for rows 16 g .. 16 g + 15 of 64
         const int d = D == 128 ? key : (lane < 16 ? wq * 16 + lane : -1);
-        if (d >= 0) {
-          int head = 0;
-          long long at = slot >= 0 ? static_cast<long long>(part) * D + d : (row0 * p.H_q + head0) * D + d;
+        int head = 0;
+        long long at = slot >= 0 ? static_cast<long long>(part) * D + d : (row0 * p.H_q + head0) * D + d;
+#pragma unroll 1
+        for (int c0 = 0; c0 < real; c0 += 16) {  // 16 columns at a time
+          float x[16];
 #pragma unroll
-          for (int q = 0; q < NQ; ++q) {
-            if (q >= real) break;
-            const float a = fac[q], b = fac[NQ + q];
-            float x = a > 0.f ? __uint_as_float(oa[q]) * a : 0.f;
-            if (b > 0.f) x += __uint_as_float(ob[q]) * b;
+          for (int q = 0; q < 16; ++q) x[q] = 0.f;
+#pragma unroll
+          for (int st = 0; st < 2; ++st) {
+            if (!(st == 0 ? have_a : have_b)) continue;
+            uint32_t hi[16];
+            tmem_ld_cols<16>(tmem + lane_addr + L::o_col(st) + c0, hi);
+            if constexpr (KV8) {
+              uint32_t lo[16];
+              tmem_ld_cols<16>(tmem + lane_addr + L::o_col(st) + NQ + c0, lo);
+#pragma unroll
+              for (int q = 0; q < 16; ++q) hi[q] = __float_as_uint(fmaf(__uint_as_float(lo[q]), L::LO, __uint_as_float(hi[q])));
+            }
+#pragma unroll
+            for (int q = 0; q < 16; ++q) {
+              const float w = fac[st * NQ + c0 + q];
+              if (w > 0.f) x[q] = fmaf(__uint_as_float(hi[q]), w, x[q]);
+            }
+          }
+          if (d < 0) continue;
+#pragma unroll
+          for (int q = 0; q < 16; ++q) {
+            if (c0 + q >= real) break;
             if (slot >= 0) {
-              p.o_part[at] = x;
+              p.o_part[at] = x[q];
               at += D;
             } else {
-              p.o[at] = __float2bfloat16(x);
+              p.o[at] = __float2bfloat16(x[q]);
               at += D;
               if (++head == p.group) {  // the next token's heads
                 head = 0;
@@ -689,6 +668,9 @@ __global__ void __launch_bounds__(FewLayout<D, KV8, NQ>::THREADS, 1)
             }
           }
         }
+        // stat and the accumulators are read (fac is this stream's own)
+        tc_fence_before();
+        if (nb > 0) mbar_arrive_warp(bar(L::B_XCHG_READ));
         group_sync(1);  // fac and stat are read by every thread of the stream before the next piece writes them
       }
       g += nb;
@@ -700,7 +682,7 @@ __global__ void __launch_bounds__(FewLayout<D, KV8, NQ>::THREADS, 1)
   // ---- teardown
   tc_fence_before();
   __syncthreads();
-  if (warp == L::WARP_MMA) {
+  if (warp == L::WARP_S) {
     tc_fence_after();
     tmem_dealloc(tmem, L::TMEM_COLS);
   }

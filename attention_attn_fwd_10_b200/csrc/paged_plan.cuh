@@ -119,64 +119,78 @@ struct PagedWalk {
   SeqWork w;          // sequence b's
 };
 
+// x / d for operands that hardly ever need 64 bits (a 64-bit division is some hundred instructions).
+__device__ __forceinline__ long long quotient(long long x, long long d) {
+  if (((x | d) >> 32) == 0) return static_cast<uint32_t>(x) / static_cast<uint32_t>(d);
+  return x / d;
+}
+
 __device__ __forceinline__ void paged_walk_start(const PagedParams& p, PagedWalk& k, int cta, int n_ctas, int lane) {
   long long total = 0;
-  for (int b0 = 0; b0 < p.n_seq; b0 += 32) {
-    SeqWork w{};
-    if (b0 + lane < p.n_seq) {
-      w = seq_work(p, b0 + lane);
-      if (w.bad && cta == 0) atomicExch(p.status, kDevBadIndex);
-    }
-    total += warp_sum(head_steps(p, w, lane)) * p.H_kv;
-  }
-  k.per = max((total + n_ctas - 1) / n_ctas, static_cast<long long>(p.min_steps));
-  k.at = min(k.per * cta, total);
-  k.end = min(k.at + k.per, total);
-  k.b = k.head = k.u = k.blk = 0;
-  if (k.at >= k.end) return;
-  long long before = 0;  // steps of the sequences before b0
-  for (int b0 = 0;; b0 += 32) {
-    SeqWork w{};
+  SeqWork w{};             // the lane's sequence of the 32 read last, its steps per head, and
+  long long per_head = 0;  // the steps of the lanes up to it (inclusive)
+  long long upto = 0;
+  auto read = [&](int b0) {
+    w = SeqWork{};
     if (b0 + lane < p.n_seq) w = seq_work(p, b0 + lane);
-    const long long per_head = head_steps(p, w, lane);
-    long long upto = per_head * p.H_kv;  // inclusive prefix over the lanes
+    per_head = head_steps(p, w, lane);
+    upto = per_head * p.H_kv;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
       const long long x = __shfl_up_sync(0xffffffffu, upto, off);
       if (lane >= off) upto += x;
     }
-    const unsigned past = __ballot_sync(0xffffffffu, before + upto > k.at);
-    if (past == 0 && b0 + 32 < p.n_seq) {
-      before += __shfl_sync(0xffffffffu, upto, 31);
-      continue;
-    }
-    const int src = past == 0 ? 31 : __ffs(past) - 1;  // (past == 0 does not happen: k.at < total)
-    const long long ph = max(1ll, __shfl_sync(0xffffffffu, per_head, src));
-    long long r = k.at - before - (__shfl_sync(0xffffffffu, upto, src) - ph * p.H_kv);
-    k.b = b0 + src;
-    k.head = static_cast<int>(r / ph);
-    r -= ph * k.head;
-    k.w = seq_work(p, min(k.b, p.n_seq - 1));
-    // the unit that holds step r of the head: 32 units at a time
-    for (int u0 = 0;; u0 += 32) {
-      const int steps = u0 + lane < k.w.units ? unit_steps(p, k.w, u0 + lane) : 0;
-      int sum = steps;
+  };
+  for (int b0 = 0; b0 < p.n_seq; b0 += 32) {
+    read(b0);
+    if (w.bad && cta == 0) atomicExch(p.status, kDevBadIndex);
+    total += __shfl_sync(0xffffffffu, upto, 31);
+  }
+  k.per = max(quotient(total + n_ctas - 1, n_ctas), static_cast<long long>(p.min_steps));
+  k.at = min(k.per * cta, total);
+  k.end = min(k.at + k.per, total);
+  k.b = k.head = k.u = k.blk = 0;
+  if (k.at >= k.end) return;
+  long long before = 0;  // steps of the sequences before b0
+  int b0 = 0;
+  while (true) {
+    if (p.n_seq > 32) read(b0);  // (32 sequences or fewer are still held)
+    if (__any_sync(0xffffffffu, before + upto > k.at) || b0 + 32 >= p.n_seq) break;
+    before += __shfl_sync(0xffffffffu, upto, 31);
+    b0 += 32;
+  }
+  const unsigned past = __ballot_sync(0xffffffffu, before + upto > k.at);
+  const int src = past == 0 ? 0 : __ffs(past) - 1;  // (never 0: k.at < total)
+  const long long ph = max(1ll, __shfl_sync(0xffffffffu, per_head, src));
+  long long r = k.at - before - (__shfl_sync(0xffffffffu, upto, src) - ph * p.H_kv);
+  k.b = b0 + src;
+  k.head = static_cast<int>(quotient(r, ph));
+  r -= ph * k.head;
+  k.w.qs = __shfl_sync(0xffffffffu, w.qs, src);
+  k.w.n_new = __shfl_sync(0xffffffffu, w.n_new, src);
+  k.w.len = __shfl_sync(0xffffffffu, w.len, src);
+  k.w.diag = __shfl_sync(0xffffffffu, w.diag, src);
+  k.w.units = __shfl_sync(0xffffffffu, w.units, src);
+  // the unit that holds step r of the head: 32 units at a time
+  for (int u0 = 0;; u0 += 32) {
+    const int steps = u0 + lane < k.w.units ? unit_steps(p, k.w, u0 + lane) : 0;
+    int sum = steps;
+    if (k.w.units > 1) {
 #pragma unroll
       for (int off = 1; off < 32; off <<= 1) {
         const int x = __shfl_up_sync(0xffffffffu, sum, off);
         if (lane >= off) sum += x;
       }
-      const unsigned in = __ballot_sync(0xffffffffu, sum > r);
-      if (in == 0 && u0 + 32 < k.w.units) {
-        r -= __shfl_sync(0xffffffffu, sum, 31);
-        continue;
-      }
-      const int lu = in == 0 ? 31 : __ffs(in) - 1;
-      k.u = u0 + lu;
-      k.blk = static_cast<int>(r - (__shfl_sync(0xffffffffu, sum, lu) - __shfl_sync(0xffffffffu, steps, lu)));
-      break;
     }
-    return;
+    const unsigned in = __ballot_sync(0xffffffffu, sum > r);
+    if (in == 0 && u0 + 32 < k.w.units) {
+      r -= __shfl_sync(0xffffffffu, sum, 31);
+      continue;
+    }
+    const int lu = in == 0 ? 0 : __ffs(in) - 1;
+    k.u = u0 + lu;
+    k.blk = static_cast<int>(r - (__shfl_sync(0xffffffffu, sum, lu) - __shfl_sync(0xffffffffu, steps, lu)));
+    break;
   }
 }
 
@@ -239,7 +253,7 @@ __device__ __forceinline__ int4 paged_cut(const PagedParams& p, const PagedWalk&
   const long long start = k.at - k.blk;
   if (start < (cta - 1) * k.per) return make_int4(-1, 0, 0, 0);
   const int q0 = k.u * p.unit_pos;
-  const long long last = (start + unit_steps(p, k.w, k.u) - 1) / k.per;
+  const long long last = quotient(start + unit_steps(p, k.w, k.u) - 1, k.per);
   return make_int4(k.w.qs + q0, min(p.unit_pos, k.w.n_new - q0), k.head, static_cast<int>(last));
 }
 
@@ -254,6 +268,7 @@ __global__ void __launch_bounds__(256) paged_merge_kernel(const PagedParams p) {
   __shared__ __align__(16) float red_o[8][D];
   __shared__ float red_m[8], red_l[8];
   // a programmatic dependent of the attention kernel: waits for its results
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int c = blockIdx.x + 1;
   const int4 cut = p.cut[c];

@@ -6,18 +6,27 @@
 
 namespace attn {
 
-// x = hi + lo, each a pair of e4m3 values (the first of a pair in the low byte).  fp16 holds the remainder
-// exactly: hi takes the leading four bits of at most eleven.
-__device__ __forceinline__ void split_e4m3x2(float x0, float x1, uint32_t& hi, uint32_t& lo) {
+// x as a sum of two e4m3 values, pairs of them in the low 16 bits (the first value in the low byte):
+//   hi = e4m3(x), lo = e4m3((x - hi) * factor).
+// fp16 holds the remainder exactly: hi takes the leading four bits of at most eleven.
+template <bool TIMES16>
+__device__ __forceinline__ void split_e4m3x2_any(float x0, float x1, uint32_t& hi, uint32_t& lo) {
   uint32_t h2, b2;
   uint16_t h, l;
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(h2) : "f"(x1), "f"(x0));
   asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(h) : "r"(h2));
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(b2) : "h"(h));
   asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(h2) : "r"(h2), "r"(b2));
+  if (TIMES16) asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(h2) : "r"(h2), "r"(0x4c004c00u));
   asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(l) : "r"(h2));
   hi = h;
   lo = l;
+}
+__device__ __forceinline__ void split_e4m3x2(float x0, float x1, uint32_t& hi, uint32_t& lo) {
+  split_e4m3x2_any<false>(x0, x1, hi, lo);
+}
+__device__ __forceinline__ void split16_e4m3x2(float x0, float x1, uint32_t& hi, uint32_t& lo) {
+  split_e4m3x2_any<true>(x0, x1, hi, lo);
 }
 
 // A query row's power of two for its e4m3 terms: `most` is the largest element's exponent field as it sits in a bf16
