@@ -260,8 +260,54 @@ __device__ __forceinline__ int4 paged_cut(const PagedParams& p, const PagedWalk&
 // Joins the pieces of the units that were cut.  Block (c, y): rows 8 y .. 8 y + 7 of the unit
 // that stretch c + 1 starts inside of: pieces 2 c + 1 and 2 c', c' = c + 1 .. last.
 //   lse = log2 sum_s 2^(lse_s),   O = sum_s 2^(lse_s - lse) O_s
-// Pieces read by warps in turn when there are many (a long sequence over many
-// CTAs), else one row per warp; the order of the sums depends on the lengths only.
+// It is a chain of reads (the record, then the pieces), so a piece's rows and log-sum-exps are asked for together:
+// up to 8 pieces by one warp per row; more (a long sequence over many CTAs) by the eight warps in turn, eight
+// at a time each, row by row.  The order of the sums depends on the lengths only.
+template <int D>
+struct MergeRow {
+  static constexpr int PER = D / 32;
+  float m = -INFINITY, sum = 0.f;
+  float acc[PER] = {};
+
+  // adds pieces first, first + step, ... below n (at most eight of them)
+  template <typename Place>
+  __device__ __forceinline__ void add(const PagedParams& p, int r, int lane, int first, int step, int n, Place place) {
+    float l[8];
+    float2 v[8][PER / 2];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int s = first + i * step;
+      l[i] = -INFINITY;
+      if (s < n) {
+        const size_t at = static_cast<size_t>(place(s)) * p.unit_rows + r;
+        l[i] = p.l_part[at];
+#pragma unroll
+        for (int x = 0; x < PER / 2; ++x) v[i][x] = reinterpret_cast<const float2*>(p.o_part + at * D + lane * PER)[x];
+      }
+    }
+    float top = m;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) top = fmaxf(top, l[i]);
+    if (top == -INFINITY) return;  // no piece so far saw a key
+    const float old = m == -INFINITY ? 0.f : exp2_mufu(m - top);
+    sum *= old;
+#pragma unroll
+    for (int x = 0; x < PER; ++x) acc[x] *= old;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (l[i] == -INFINITY) continue;
+      const float w = exp2_mufu(l[i] - top);
+      sum += w;
+#pragma unroll
+      for (int x = 0; x < PER / 2; ++x) {
+        acc[2 * x] += w * v[i][x].x;
+        acc[2 * x + 1] += w * v[i][x].y;
+      }
+    }
+    m = top;
+  }
+};
+
 template <int D, int TILE_ROWS>
 __global__ void __launch_bounds__(256) paged_merge_kernel(const PagedParams p) {
   constexpr int PER = D / 32;
@@ -284,69 +330,46 @@ __global__ void __launch_bounds__(256) paged_merge_kernel(const PagedParams p) {
     const int pos = r / TILE_ROWS * p.tile_pos + rr / p.group;
     const bool valid = rr < p.group * p.tile_pos && pos < cut.y;
     if (!valid) continue;  // (the same for the whole block when wide)
-    const int first = wide ? warp : 0, step = wide ? 8 : 1;
-    float m = -INFINITY;
-    for (int s = first + lane * step; s < n; s += 32 * step)
-      m = fmaxf(m, p.l_part[static_cast<size_t>(place(s)) * p.unit_rows + r]);
+    MergeRow<D> row;
+    if (!wide) {
+      row.add(p, r, lane, 0, 1, n, place);
+    } else {
+      for (int s = warp; s < n; s += 64) row.add(p, r, lane, s, 8, n, place);
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
-    float acc[PER], sum = 0.f;
-#pragma unroll
-    for (int x = 0; x < PER; ++x) acc[x] = 0.f;
-    if (m > -INFINITY) {
-#pragma unroll 4
-      for (int s = first; s < n; s += step) {
-        const size_t at = static_cast<size_t>(place(s)) * p.unit_rows + r;
-        const float l = p.l_part[at];
-        const float wgt = exp2_mufu(l - m);  // 0 for a piece that saw no key
-        const float* src = p.o_part + at * D + lane * PER;
-        sum += wgt;
-#pragma unroll
-        for (int x = 0; x < PER / 2; ++x) {
-          const float2 v = reinterpret_cast<const float2*>(src)[x];
-          acc[2 * x] += wgt * v.x;
-          acc[2 * x + 1] += wgt * v.y;
-        }
-      }
-    }
-    if (wide) {
-#pragma unroll
-      for (int x = 0; x < PER; ++x) red_o[warp][lane * PER + x] = acc[x];
+      for (int x = 0; x < PER; ++x) red_o[warp][lane * PER + x] = row.acc[x];
       if (lane == 0) {
-        red_m[warp] = m;
-        red_l[warp] = sum;
+        red_m[warp] = row.m;
+        red_l[warp] = row.sum;
       }
       __syncthreads();
       if (warp == 0) {
-        float mm = red_m[0];
+        float top = red_m[0];
 #pragma unroll
-        for (int g = 1; g < 8; ++g) mm = fmaxf(mm, red_m[g]);
-        sum = 0.f;
-#pragma unroll
-        for (int x = 0; x < PER; ++x) acc[x] = 0.f;
-        if (mm > -INFINITY) {
+        for (int g = 1; g < 8; ++g) top = fmaxf(top, red_m[g]);
+        row = MergeRow<D>{};
+        row.m = top;
+        if (top > -INFINITY) {
 #pragma unroll
           for (int g = 0; g < 8; ++g) {
-            const float wgt = exp2_mufu(red_m[g] - mm);
-            sum += wgt * red_l[g];
+            const float w = exp2_mufu(red_m[g] - top);
+            row.sum += w * red_l[g];
 #pragma unroll
-            for (int x = 0; x < PER; ++x) acc[x] += wgt * red_o[g][lane * PER + x];
+            for (int x = 0; x < PER; ++x) row.acc[x] += w * red_o[g][lane * PER + x];
           }
         }
-        m = mm;
       }
       __syncthreads();
       if (warp != 0) continue;
     }
-    const float inv = sum > 0.f ? 1.f / sum : 0.f;
+    const float inv = row.sum > 0.f ? 1.f / row.sum : 0.f;
     const int h = cut.z * p.group + rr % p.group;
-    const long long row = static_cast<long long>(cut.x) + pos;
-    uint32_t* dst = reinterpret_cast<uint32_t*>(p.o + (row * p.H_q + h) * D + lane * PER);
+    const long long at = static_cast<long long>(cut.x) + pos;
+    uint32_t* dst = reinterpret_cast<uint32_t*>(p.o + (at * p.H_q + h) * D + lane * PER);
 #pragma unroll
-    for (int x = 0; x < PER / 2; ++x) dst[x] = pack_bf16x2(acc[2 * x] * inv, acc[2 * x + 1] * inv);
+    for (int x = 0; x < PER / 2; ++x) dst[x] = pack_bf16x2(row.acc[2 * x] * inv, row.acc[2 * x + 1] * inv);
     if (lane == 0)
-      p.lse[static_cast<long long>(h) * p.n_tokens + row] =
-          sum > 0.f ? (m + log2f(sum)) * 0.69314718055994531f : -INFINITY;
+      p.lse[static_cast<long long>(h) * p.n_tokens + at] =
+          row.sum > 0.f ? (row.m + log2f(row.sum)) * 0.69314718055994531f : -INFINITY;
   }
 }
 

@@ -23,6 +23,13 @@ from ._abi import load
 __all__ = ["Rotary", "PagedKV", "rope", "paged_append", "fwd_paged", "fwd_paged_workspace_size"]
 
 _SAME = contextlib.nullcontext()
+# The raw handle of a device's current stream, without the object around it (a call is a few microseconds).
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
+def _like(t, dev):
+    """An uninitialised dense tensor of t's shape and type."""
+    return torch.empty_like(t) if t.is_contiguous() else torch.empty(t.shape, dtype=t.dtype, device=dev)
 
 
 def _scope(stream, dev: torch.device):
@@ -76,6 +83,7 @@ class Rotary:
         if not 1 <= len(sections) <= 4 or min(sections) < 0 or sum(sections) != n:
             raise ValueError(f"sections {sections} must be 1 to 4 counts that sum to {n}")
         self.inv_freq, self.sections, self.interleaved = inv_freq, sections, bool(interleaved)
+        self._section = (ctypes.c_int * 4)(*sections)
 
     @property
     def device(self):
@@ -96,7 +104,7 @@ class Rotary:
         elif len(self.sections) > 1:
             raise ValueError("several axes need positions")
         return _abi.RotaryStruct(self.inv_freq.data_ptr(), ptr, self.inv_freq.numel(), len(self.sections),
-                                 (ctypes.c_int * 4)(*self.sections), int(self.interleaved))
+                                 self._section, int(self.interleaved))
 
 
 def rope(q, k=None, *, rotary: Rotary, positions=None, inverse: bool = False, q_out=None, k_out=None, stream=None):
@@ -123,18 +131,20 @@ def rope(q, k=None, *, rotary: Rotary, positions=None, inverse: bool = False, q_
     r = rotary._struct(positions, tokens, dev)
     with _scope(stream, dev):
         if q_out is None:
-            q_out = torch.empty(q.shape, dtype=q.dtype, device=dev)
-        qo_step = _rows("q_out", q_out, dev)[3]
+            q_out, qo_step = _like(q, dev), H_q * D
+        else:
+            qo_step = _rows("q_out", q_out, dev)[3]
         if k is not None:
             if k_out is None:
-                k_out = torch.empty(k.shape, dtype=k.dtype, device=dev)
-            ko_step = _rows("k_out", k_out, dev)[3]
+                k_out, ko_step = _like(k, dev), H_k * D
+            else:
+                ko_step = _rows("k_out", k_out, dev)[3]
         if tokens == 0:
             return q_out if k is None else (q_out, k_out)
         code = load().attn_rope(q.data_ptr(), None if k is None else k.data_ptr(), q_out.data_ptr(),
                                 None if k is None else k_out.data_ptr(), tokens, H_q, H_k, D, q_step, k_step, qo_step,
                                 ko_step, max(period, 1), ctypes.byref(r), int(bool(inverse)),
-                                torch.cuda.current_stream().cuda_stream)
+                                _raw_stream(dev.index))
     _abi.check(code, "attn_rope")
     return q_out if k is None else (q_out, k_out)
 
@@ -214,12 +224,12 @@ def paged_append(cache: PagedKV, k, v, q=None, rotary: Rotary | None = None, pos
     r = None if rotary is None else ctypes.byref(rotary._struct(positions, tokens, dev))
     with _scope(stream, dev):
         if q is not None and q_out is None:
-            q_out = torch.empty(q.shape, dtype=q.dtype, device=dev)
+            q_out = _like(q, dev)
         if tokens == 0:
             return q_out
         code = load().attn_paged_append(cache._ref, None if q is None else q.data_ptr(), k.data_ptr(), v.data_ptr(),
                                         None if q is None else q_out.data_ptr(), tokens, H_q, q_step, k_step, v_step,
-                                        r, torch.cuda.current_stream().cuda_stream)
+                                        r, _raw_stream(dev.index))
     _abi.check(code, "attn_paged_append")
     return q_out
 
@@ -257,9 +267,9 @@ def fwd_paged(cache: PagedKV, q, causal: bool = True, scale: float | None = None
         raise ValueError(f"workspace must be a contiguous buffer of at least {need} bytes on {dev}")
     with _scope(stream, dev):
         if out is None:
-            out = torch.empty((tokens, H_q, D), dtype=torch.bfloat16, device=dev)
+            out = _like(q, dev)
         if lse is None:
-            lse = torch.empty((H_q, tokens), dtype=torch.float32, device=dev)
+            lse = torch.empty_strided((H_q, tokens), (tokens, 1), dtype=torch.float32, device=dev)
         if workspace is None:
             workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
         if tokens == 0:
@@ -267,6 +277,6 @@ def fwd_paged(cache: PagedKV, q, causal: bool = True, scale: float | None = None
         code = load().attn_fwd_paged(cache._ref, q.data_ptr(), out.data_ptr(), lse.data_ptr(), workspace.data_ptr(),
                                      tokens, H_q, q_step, int(max_new), int(bool(causal)),
                                      1.0 / math.sqrt(D) if scale is None else float(scale),
-                                     torch.cuda.current_stream().cuda_stream)
+                                     _raw_stream(dev.index))
     _abi.check(code, "attn_fwd_paged")
     return out, lse
