@@ -221,7 +221,7 @@ cudaError_t launch_paged(void (*kern)(CUtensorMap, CUtensorMap, CUtensorMap, Pag
   if (e != cudaSuccess) return e;
   e = launch_dependent(kern, dim3(kPagedCtas), L::THREADS, L::SMEM_BYTES, s, mq, mk, mv, p);
   if (e != cudaSuccess) return e;
-  return launch_dependent(paged_merge_kernel<D, TILE_ROWS>, dim3(kPagedCtas - 1, static_cast<unsigned>((p.unit_rows + 7) / 8)),
+  return launch_dependent(paged_merge_kernel<D, TILE_ROWS>, dim3(kPagedCtas - 1, static_cast<unsigned>(p.unit_rows / (8 * merge_rows(TILE_ROWS)))),
                           256, 0, s, p);
 }
 

@@ -20,14 +20,14 @@
 // A piece whose tokens fit one tile runs as two streams: tile 0 takes its even and tile 1 its
 // odd blocks for the same rows, and tile 0 joins both.
 //
-// e4m3 cache: both products run as kind::f8f6f4 with the 16-bit operand as a sum of two e4m3 terms,
-//   x = hi + lo,  hi = e4m3(x), lo = e4m3(x - hi):
-// the remainder of a bf16 after hi is a multiple of its last bit of at most 8 such
-// steps, so q (scaled per row by a power of two into e4m3's range) is represented exactly down to 2^-17 of
-// the row's largest element, and p within 2^-8.  Two MMAs at twice the rate cost what one bf16
-// MMA does, and K and V stay at one byte in memory, in L2 and in shared memory.
-// The largest p of a row is kept in 2^7 .. 2^8 (SHIFT, TAU): e4m3's smallest step is 2^-9, so a small weight
-// is off by at most 2^-17 of the largest.
+// e4m3 cache: S runs as kind::f8f6f4 with q as a sum of two e4m3 terms,
+//   q = hi + lo,  hi = e4m3(q), lo = e4m3(q - hi):
+// the remainder of a bf16 after hi is a multiple of its last bit of at most 8 such steps, so q (scaled per row by a
+// power of two into e4m3's range) is represented exactly down to 2^-17 of the row's largest element; two
+// MMAs at twice the rate cost what one bf16 MMA does.  The softmax weights are fp16 and V is turned into
+// fp16 in shared memory (exactly) by four more warps, 12-15: 128 x D values a block, where splitting the weights as
+// well would take 256 x 128 and the time of the busiest warps (a block of two tiles, D = 64: 4.3k clk of softmax
+// instead of 2.1k).
 #pragma once
 
 #include <cuda_fp16.h>
@@ -49,12 +49,16 @@ struct ChunkLayout {
   static constexpr int KV_BYTES = NBOX * BOX_BYTES;      // a K or V tile
   // bf16: a Q tile is NBOX box columns; e4m3: the hi and the lo tile
   static constexpr int Q_BYTES = KV8 ? 2 * KV_BYTES : KV_BYTES;
-  static constexpr int KST = KV8 ? 5 : (D == 128 ? 3 : 5);
-  static constexpr int VST = KV8 ? 4 : (D == 128 ? 2 : 4);
+  static constexpr int KST = KV8 ? (D == 128 ? 4 : 5) : (D == 128 ? 3 : 5);
+  static constexpr int VST = KV8 ? (D == 128 ? 2 : 4) : (D == 128 ? 2 : 4);
+  // V as the MMA reads it: D / 64 columns of 128-byte rows of 16-bit values (e4m3: written by the converters)
+  static constexpr int VM_BYTES = 128 * D * 2;
+  static constexpr int VMST = KV8 ? 2 : VST;
   static constexpr int Q_OFF = 0;
   static constexpr int K_OFF = 2 * Q_BYTES;
-  static constexpr int V_OFF = K_OFF + KST * KV_BYTES;
-  static constexpr int BAR_OFF = V_OFF + VST * KV_BYTES;
+  static constexpr int V_OFF = K_OFF + KST * KV_BYTES;   // as loaded
+  static constexpr int VM_OFF = KV8 ? V_OFF + VST * KV_BYTES : V_OFF;
+  static constexpr int BAR_OFF = VM_OFF + VMST * VM_BYTES;
   static constexpr int NI = 4;  // work item ring
   static constexpr int B_Q_FULL = 0;                 // [t]
   static constexpr int B_Q_EMPTY = B_Q_FULL + 2;     // [t]
@@ -62,8 +66,10 @@ struct ChunkLayout {
   static constexpr int B_K_EMPTY = B_K_FULL + KST;
   static constexpr int B_V_FULL = B_K_EMPTY + KST;   // [VST]
   static constexpr int B_V_EMPTY = B_V_FULL + VST;
-  static constexpr int B_V_RAW = B_V_EMPTY + VST;    // a block to be mended before V_FULL
-  static constexpr int B_S_FULL = B_V_RAW + 1;       // [t]
+  static constexpr int B_V_RAW = B_V_EMPTY + VST;    // bf16: a block to be mended before V_FULL
+  static constexpr int B_VM_FULL = B_V_RAW + 1;      // [VMST] e4m3: converted (four warps)
+  static constexpr int B_VM_EMPTY = B_VM_FULL + VMST;
+  static constexpr int B_S_FULL = B_VM_EMPTY + VMST; // [t]
   static constexpr int B_P_FULL = B_S_FULL + 2;      // [t][half]
   static constexpr int B_O_FINAL = B_P_FULL + 4;     // [t]
   static constexpr int B_XCHG = B_O_FINAL + 2;
@@ -72,7 +78,7 @@ struct ChunkLayout {
   static constexpr int B_ITEM_EMPTY = B_ITEM_FULL + NI;
   static constexpr int B_DRAIN = B_ITEM_EMPTY + NI;
   static constexpr int N_BARS = B_DRAIN + 1;
-  static constexpr int ITEM_READERS = 11;  // 8 softmax warps, two producers, the issuer
+  static constexpr int ITEM_READERS = KV8 ? 15 : 11;  // 8 softmax warps, two producers, the issuer, 4 converters
   static constexpr int XCHG_OFF = BAR_OFF + (8 * N_BARS + 15) / 16 * 16;  // two streams: tile 1's row statistics
   static constexpr int ITEM_OFF = XCHG_OFF + 1024;
   static constexpr int TMEM_SLOT_OFF = ITEM_OFF + NI * static_cast<int>(sizeof(PagedItem));
@@ -84,14 +90,14 @@ struct ChunkLayout {
   __device__ static constexpr uint32_t s_col(int t) { return static_cast<uint32_t>(t) * 128u; }
   __device__ static constexpr uint32_t o_col(int t) { return 256u + static_cast<uint32_t>(t) * D; }
   static constexpr uint32_t TMEM_COLS = 512;
-  static constexpr int THREADS = 384;
+  static constexpr int THREADS = KV8 ? 512 : 384;
   static constexpr int WARP_K = 8, WARP_MMA = 9, WARP_V = 10, WARP_SCHED = 11;
-  static constexpr int REG_SOFTMAX = 216, REG_OTHER = 72;  // 2 x 128 x 216 + 128 x 72 = 384 x 168
-  // e4m3: weights up to 2^(SHIFT + TAU) = 2^8 < 448
-  static constexpr float SHIFT = KV8 ? 7.f : 0.f;
-  static constexpr float TAU = KV8 ? 1.f : 8.f;
-  // shared-memory descriptor of a K-major operand, and of V (MN-major)
+  // 2 x 128 x 216 + 128 x 72 = 384 x 168; e4m3: 2 x 128 x 200 + 256 x 56 = 512 x 128
+  static constexpr int REG_LAUNCH = KV8 ? 128 : 168, REG_SOFTMAX = KV8 ? 200 : 216, REG_OTHER = KV8 ? 56 : 72;
+  static constexpr float TAU = 8.f;  // weights stay below 2^TAU
+  // shared-memory descriptors' high half: K-major Q and K, and V (MN-major)
   static constexpr uint32_t HI = ROW_BYTES == 128 ? sdesc_sw128_hi(1024) : sdesc_sw64_hi(512);
+  static constexpr uint32_t HI_V = sdesc_sw128_hi(1024);
 };
 
 // A query row (bf16, D values in w) as hi and lo e4m3 terms, scaled by the power of two that puts its largest
@@ -127,16 +133,14 @@ __device__ __forceinline__ float q_row_to_e4m3x2(const uint4* w, int row, uint8_
   return q_factor(scale_log2, up);
 }
 
-// p = 2^(s c - m) for 64 of a row's columns (exp_half's layout), as two e4m3 terms: words 0 .. 15 of pk hold the
-// hi terms (four columns a word), 16 .. 31 the lo terms; returns the fp32 sum of the unrounded p.
+// exp_half (fwd_kernel.cuh) with the weights as fp16 pairs.
 template <int POLY_EVERY>
-__device__ __forceinline__ float exp_half_e4m3x2(const uint32_t* sr, float c, float m, uint32_t* pk, int half) {
+__device__ __forceinline__ float exp_half_f16(const uint32_t* sr, float c, float m, uint32_t* pk, int half) {
   const uint64_t c2 = f2_pack(c, c);
   const uint64_t nm2 = f2_pack(-m, -m);
   uint64_t acc[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) acc[i] = 0ull;
-  uint32_t hi0 = 0, lo0 = 0;
 #pragma unroll
   for (int q = 0; q < 32; ++q) {
     const int cp = 32 * half + q;
@@ -150,14 +154,7 @@ __device__ __forceinline__ float exp_half_e4m3x2(const uint32_t* sr, float c, fl
       e1 = exp2_mufu(x1);
     }
     acc[q & 3] = f2_add(acc[q & 3], f2_pack(e0, e1));
-    uint32_t hi, lo;
-    split_e4m3x2(e0, e1, hi, lo);
-    if (q & 1) {
-      pk[q >> 1] = hi0 | (hi << 16);
-      pk[16 + (q >> 1)] = lo0 | (lo << 16);
-    }
-    hi0 = hi;
-    lo0 = lo;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(pk[q]) : "f"(e1), "f"(e0));
   }
   float a0, a1;
   f2_unpack(f2_add(f2_add(acc[0], acc[1]), f2_add(acc[2], acc[3])), a0, a1);
@@ -187,6 +184,8 @@ __global__ void __launch_bounds__(ChunkLayout<D, KV8>::THREADS, 1)
       uint32_t n = 1;
       if ((i >= L::B_P_FULL && i < L::B_P_FULL + 4) || i == L::B_XCHG || i == L::B_XCHG_READ) n = 4;
       if (KV8 && i >= L::B_Q_FULL && i < L::B_Q_FULL + 2) n = 4;  // written by the four warps of a tile
+      if (KV8 && i >= L::B_V_EMPTY && i < L::B_V_EMPTY + L::VST) n = 4;     // read by the converters
+      if (KV8 && i >= L::B_VM_FULL && i < L::B_VM_FULL + L::VMST) n = 4;
       if (i >= L::B_ITEM_EMPTY && i < L::B_ITEM_EMPTY + L::NI) n = L::ITEM_READERS;
       mbar_init(bar(i), n);
     }
@@ -213,7 +212,8 @@ __global__ void __launch_bounds__(ChunkLayout<D, KV8>::THREADS, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(sptr + L::TMEM_SLOT_OFF);
-  static_assert(2 * 128 * L::REG_SOFTMAX + 128 * L::REG_OTHER <= L::THREADS * 168, "register split");
+  static_assert(2 * 128 * L::REG_SOFTMAX + (L::THREADS - 256) * L::REG_OTHER <= L::THREADS * L::REG_LAUNCH,
+                "register split");
 
   // Piece u of the CTA sits in ring slot u % NI once ITEM_FULL completes; every reader arrives on
   // ITEM_EMPTY when it needs it no more.
@@ -287,7 +287,7 @@ __global__ void __launch_bounds__(ChunkLayout<D, KV8>::THREADS, 1)
           break;
         const uint32_t dst = sbase + L::V_OFF + s * L::KV_BYTES;
         const int live = len - (j0 + j) * L::BN;  // keys of the block that the sequence has
-        if (live >= L::BN) {
+        if (KV8 || live >= L::BN) {
           load_block<L::NBOX, L::ROW_BYTES>(p, &tm_v, dst, bar(L::B_V_FULL + s), win, seq, head, len, j0 + j, lane);
         } else {
           load_block<L::NBOX, L::ROW_BYTES>(p, &tm_v, dst, bar(L::B_V_RAW), win, seq, head, len, j0 + j, lane);
@@ -311,7 +311,8 @@ __global__ void __launch_bounds__(ChunkLayout<D, KV8>::THREADS, 1)
     // ===================== MMA issuer =====================
     if (lane == 0) {
       constexpr uint32_t IDESC_S = KV8 ? idesc_e4m3_f32(128, 128) : idesc_bf16_f32(128, 128, false, false);
-      constexpr uint32_t IDESC_PV = KV8 ? (idesc_e4m3_f32(128, D) | (1u << 16)) : idesc_bf16_f32(128, D, false, true);
+      // (bf16's type codes are 1, fp16's 0)
+      constexpr uint32_t IDESC_PV = idesc_bf16_f32(128, D, false, true) & ~(KV8 ? (1u << 7) | (1u << 10) : 0u);
       auto opaque = [](uint32_t x) {  // keeps the descriptors' arithmetic where it is used (72 registers)
         uint32_t y;
         asm volatile("mov.b32 %0, %1;" : "=r"(y) : "r"(x));
@@ -339,25 +340,16 @@ __global__ void __launch_bounds__(ChunkLayout<D, KV8>::THREADS, 1)
       };
       // PV_t(j) in two halves of 64 keys, each issued once its half of P_t(j) is in tensor memory
       auto issue_pv_half = [&](int t, int stage, bool acc, int hf) {
-        const uint32_t v_base = opaque(sbase) + L::V_OFF + stage * L::KV_BYTES;
-        if constexpr (KV8) {
-          const uint32_t vd = sdesc_lo(v_base, 16);
+        const uint32_t vd = sdesc_lo(opaque(sbase) + L::VM_OFF + stage * L::VM_BYTES, 128 * 128);
 #pragma unroll
-          for (int k2 = 0; k2 < 4; ++k2) {  // 32 keys an MMA: two of the hi terms, two of the lo terms
-            const int kk = 2 * hf + (k2 & 1);
-            umma_ts_f8_h(tmem + L::o_col(t), tmem + L::s_col(t) + 32 * (k2 >> 1) + kk * 8, vd + (kk * 32 * L::ROW_BYTES >> 4),
-                         L::HI, IDESC_PV, (acc || hf > 0 || k2 > 0) ? 1u : 0u);
-          }
-        } else {
-          const uint32_t vd = sdesc_lo(v_base, L::BOX_BYTES);
-#pragma unroll
-          for (int k4 = 0; k4 < 4; ++k4) {
-            const int kk = 4 * hf + k4;
-            umma_ts_h(tmem + L::o_col(t), tmem + L::s_col(t) + kk * 8, vd + (kk * 2048 >> 4), L::HI, IDESC_PV,
-                      (acc || kk > 0) ? 1u : 0u);
-          }
+        for (int k4 = 0; k4 < 4; ++k4) {
+          const int kk = 4 * hf + k4;  // 16 keys
+          umma_ts_h(tmem + L::o_col(t), tmem + L::s_col(t) + kk * 8, vd + (kk * 2048 >> 4), L::HI_V, IDESC_PV,
+                    (acc || kk > 0) ? 1u : 0u);
         }
       };
+      // V as the MMAs read it: loaded (bf16), converted (e4m3)
+      constexpr int V_READY = KV8 ? L::B_VM_FULL : L::B_V_FULL, V_USED = KV8 ? L::B_VM_EMPTY : L::B_V_EMPTY;
       int kc = 0, vc = 0, qc0 = 0, qc1 = 0, pc0 = 0, pc1 = 0;
       bool ok = true;
       for (int u = 0; ok; ++u) {
@@ -387,9 +379,9 @@ __global__ void __launch_bounds__(ChunkLayout<D, KV8>::THREADS, 1)
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
               if (!ok || j >= nblk(t)) continue;
-              const int vs = vc % L::VST;
+              const int vs = vc % L::VMST;
               const int ph = ((t == 0 ? pc0 : pc1) + j) & 1;
-              ok = mbar_wait(bar(L::B_V_FULL + vs), (vc / L::VST) & 1, ctl);
+              ok = mbar_wait(bar(V_READY + vs), (vc / L::VMST) & 1, ctl);
               ok = ok && mbar_wait(bar(L::B_P_FULL + 2 * t), ph, ctl);
               if (!ok) break;
               tc_fence_after();
@@ -398,7 +390,7 @@ __global__ void __launch_bounds__(ChunkLayout<D, KV8>::THREADS, 1)
               tc_fence_after();
               issue_pv_half(t, vs, j > 0, 1);
               if (j == nblk(t) - 1) umma_commit(bar(L::B_O_FINAL + t));
-              umma_commit(bar(L::B_V_EMPTY + vs));
+              umma_commit(bar(V_USED + vs));
               ++vc;
               if (j + 1 < nblk(t)) {
                 const int ks = kc % L::KST;
@@ -426,9 +418,9 @@ __global__ void __launch_bounds__(ChunkLayout<D, KV8>::THREADS, 1)
           // per block: PV_0(j), S_0(j+1), PV_1(j), S_1(j+1); MMAs of one thread run in issue order, so PV_t(j) has
           // read P_t(j) before S_t(j+1) overwrites it
           for (int j = 0; ok && j < n_blocks; ++j) {
-            const int vs = vc % L::VST;
+            const int vs = vc % L::VMST;
             const int ks = kc % L::KST;
-            if (!(ok = mbar_wait(bar(L::B_V_FULL + vs), (vc / L::VST) & 1, ctl))) break;
+            if (!(ok = mbar_wait(bar(V_READY + vs), (vc / L::VMST) & 1, ctl))) break;
             bool k_next = false;
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
@@ -451,7 +443,7 @@ __global__ void __launch_bounds__(ChunkLayout<D, KV8>::THREADS, 1)
               }
             }
             if (!ok) break;
-            umma_commit(bar(L::B_V_EMPTY + vs));
+            umma_commit(bar(V_USED + vs));
             ++vc;
             if (k_next) {
               umma_commit(bar(L::B_K_EMPTY + ks));
@@ -481,6 +473,51 @@ __global__ void __launch_bounds__(ChunkLayout<D, KV8>::THREADS, 1)
         mbar_arrive(bar(L::B_ITEM_FULL + u % L::NI));
       }
       if (it.row0 < 0) break;
+    }
+  } else if (KV8 && warp >= 12) {
+    // ===================== converters: V from e4m3 to fp16 =====================
+    const int tid = threadIdx.x - 384;
+    int n = 0;
+    bool ok = true;
+    for (int u = 0; ok; ++u) {
+      if (!(ok = __all_sync(0xffffffffu, wait_item(u)))) break;
+      const volatile PagedItem* it = item_at(u);
+      const int row0 = it->row0, len = it->len, j0 = it->j0, n_loads = it->n_loads;
+      mbar_arrive_warp(item_done(u));
+      if (row0 < 0) break;
+      for (int j = 0; j < n_loads; ++j, ++n) {
+        const int s = n % L::VST, sm = n % L::VMST;
+        ok = mbar_wait(bar(L::B_V_FULL + s), (n / L::VST) & 1, ctl);
+        if (ok && n >= L::VMST) ok = mbar_wait(bar(L::B_VM_EMPTY + sm), ((n / L::VMST) - 1) & 1, ctl);
+        if (!(ok = __all_sync(0xffffffffu, ok))) break;
+        const int live = len - (j0 + j) * L::BN;  // rows past the sequence's end become zeros
+        const uint8_t* src = sptr + L::V_OFF + s * L::KV_BYTES;
+        uint8_t* dst = sptr + L::VM_OFF + sm * L::VM_BYTES;
+        // 16 dims of a key at a time: a 16-byte chunk in, two out
+        constexpr int CHUNKS = D / 16;
+#pragma unroll
+        for (int i = 0; i < CHUNKS; ++i) {
+          const int e = i * 128 + tid, key = e / CHUNKS, c = e % CHUNKS;
+          const int sw = L::ROW_BYTES == 128 ? (key & 7) : ((key >> 1) & 3);
+          const uint4 x = *reinterpret_cast<const uint4*>(src + key * L::ROW_BYTES + ((c ^ sw) * 16));
+          const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+          uint32_t y[8];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(y[2 * k]) : "h"(static_cast<uint16_t>(w[k])));
+            asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(y[2 * k + 1]) : "h"(static_cast<uint16_t>(w[k] >> 16)));
+          }
+          const bool in = key < live;
+          uint8_t* row = dst + (c >> 2) * (128 * 128) + key * 128;
+          *reinterpret_cast<uint4*>(row + (((2 * c) & 7) ^ (key & 7)) * 16) =
+              in ? make_uint4(y[0], y[1], y[2], y[3]) : make_uint4(0, 0, 0, 0);
+          *reinterpret_cast<uint4*>(row + (((2 * c + 1) & 7) ^ (key & 7)) * 16) =
+              in ? make_uint4(y[4], y[5], y[6], y[7]) : make_uint4(0, 0, 0, 0);
+        }
+        fence_proxy_async_smem();
+        mbar_arrive_warp(bar(L::B_VM_FULL + sm));
+        mbar_arrive_warp(bar(L::B_V_EMPTY + s));
+      }
     }
   } else {
     // ===================== softmax warpgroups =====================
@@ -552,7 +589,7 @@ __global__ void __launch_bounds__(ChunkLayout<D, KV8>::THREADS, 1)
             if (cc > lim_c) s[cc] = -INFINITY;
         }
         const float mx = row_max128(sr);
-        const float m_new = fmaxf(m_used, mx * c - L::SHIFT);
+        const float m_new = fmaxf(m_used, mx * c);
         const bool resc = (m_new - m_used) > L::TAU;  // false for NaN (-inf - -inf)
         float alpha = 1.f;
         if (resc) {
@@ -577,13 +614,11 @@ __global__ void __launch_bounds__(ChunkLayout<D, KV8>::THREADS, 1)
         for (int hf = 0; hf < 2; ++hf) {
           uint32_t pk[32];
           if constexpr (KV8) {
-            l += need_mask ? exp_half_e4m3x2<0>(sr, c, m_eff, pk, hf) : exp_half_e4m3x2<8>(sr, c, m_eff, pk, hf);
-            tmem_st16(s_addr + 16 * hf, pk);
-            tmem_st16(s_addr + 32 + 16 * hf, pk + 16);
+            l += need_mask ? exp_half_f16<0>(sr, c, m_eff, pk, hf) : exp_half_f16<8>(sr, c, m_eff, pk, hf);
           } else {
             l += need_mask ? exp_half<0>(sr, c, m_eff, pk, hf) : exp_half<8>(sr, c, m_eff, pk, hf);
-            tmem_st32(s_addr + 32 * hf, pk);
           }
+          tmem_st32(s_addr + 32 * hf, pk);
           tmem_st_wait();
           tc_fence_before();
           mbar_arrive_warp(bar(L::B_P_FULL + 2 * t + hf));
@@ -648,9 +683,10 @@ __global__ void __launch_bounds__(ChunkLayout<D, KV8>::THREADS, 1)
             }
             if (!valid) continue;
             if (slot >= 0) {
-              float4* dst = reinterpret_cast<float4*>(p.o_part + part * D + ch * 16);
-#pragma unroll
-              for (int i = 0; i < 4; ++i) dst[i] = make_float4(ov[4 * i], ov[4 * i + 1], ov[4 * i + 2], ov[4 * i + 3]);
+              // (256-bit stores: a row chunk's whole sectors at once)
+              float* dst = p.o_part + part * D + ch * 16;
+              st_global_v8(dst, orr);
+              st_global_v8(dst + 8, orr + 8);
             } else {
               uint32_t pkd[8];
 #pragma unroll

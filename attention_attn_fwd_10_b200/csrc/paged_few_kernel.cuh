@@ -20,7 +20,7 @@
 //
 // An MMA of M = 128 and N <= 32 takes 46 clk whatever N is (65 at N = 128), and issuing one about as long: with
 // one issuing thread for both products a block took 1800 clk.  e4m3 cache: q and the weights are sums of two
-// e4m3 terms (as in the chunk kernel), which stand side by side as 2 NQ columns of the same MMAs --
+// e4m3 terms (x = hi + lo, hi = e4m3(x), lo = e4m3(x - hi): 8 bits of x), which stand side by side as 2 NQ columns of the same MMAs --
 // half the MMAs of two passes -- and are added in the softmax and in the epilogue.  The low terms carry a factor
 // of 16, so a weight's floor is 2^-14: with a row's largest weight at 2^SHIFT or more, 2^-17 of it.
 #pragma once

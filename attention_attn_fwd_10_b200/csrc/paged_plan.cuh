@@ -2,16 +2,20 @@
 //
 // Lengths are read when the call runs, so the host cannot lay the work out.  A
 // unit is up to `unit_pos` new tokens of one sequence and the query heads of
-// one kv head; its steps are the 128-key blocks its last token sees (one step
-// where it sees none: its rows still get their zeros).  All units' steps form one
-// line, ordered by sequence, kv head, unit; CTA c takes the c-th of gridDim.x
-// equal stretches, so the loads are even whatever the lengths: a ragged batch, one long
+// one kv head; its steps are the 128-key blocks its last token sees (one block
+// where it sees none: its rows still get their zeros), two steps a block where both
+// tiles work on it and one where the tokens fit one tile (a block of the chunk kernel takes 2.9 us for two
+// tiles, 1.2 us for one).  All units' steps form one
+// line, ordered by sequence, kv head, unit, each with an even number; CTA c takes the c-th of gridDim.x
+// equal stretches (of even length: no block is cut), so the loads are even whatever the lengths: a ragged batch, one long
 // sequence, chunks beside single tokens.  A unit cut by a stretch's end is
 // computed in pieces, each left in the workspace as fp32 rows normalized over
 // the piece's keys with their log-sum-exp, and joined by paged_merge_kernel.
 // Every CTA finds its stretch by itself from the index arrays (two passes of 32
 // sequences at a time): no planning launch and no state between calls.
 #pragma once
+
+#include <type_traits>
 
 #include "rotary_kernels.cuh"
 #include "sm100_common.cuh"
@@ -79,8 +83,13 @@ __device__ __forceinline__ int blocks_to(const PagedParams& p, const SeqWork& w,
   const int last = p.causal ? min(min(end, w.n_new) - 1 + w.diag, w.len - 1) : w.len - 1;
   return last < 0 ? 0 : (last >> 7) + 1;
 }
+// Whether unit u's tokens fit one tile.
+__device__ __forceinline__ bool one_tile(const PagedParams& p, const SeqWork& w, int u) {
+  return w.n_new - u * p.unit_pos <= p.tile_pos;
+}
 __device__ __forceinline__ int unit_steps(const PagedParams& p, const SeqWork& w, int u) {
-  return max(1, blocks_to(p, w, (u + 1) * p.unit_pos));
+  const int blocks = max(1, blocks_to(p, w, (u + 1) * p.unit_pos));
+  return one_tile(p, w, u) ? (blocks + 1) & ~1 : 2 * blocks;
 }
 
 __device__ __forceinline__ long long warp_sum(long long x) {
@@ -115,7 +124,7 @@ __device__ __forceinline__ long long head_steps(const PagedParams& p, const SeqW
 struct PagedWalk {
   long long at, end;  // next step, end of the stretch
   long long per;      // steps of a stretch
-  int b, head, u, blk;  // where `at` is: sequence, kv head, unit, block of the unit
+  int b, head, u, step;  // where `at` is: sequence, kv head, unit, step of the unit
   SeqWork w;          // sequence b's
 };
 
@@ -146,10 +155,10 @@ __device__ __forceinline__ void paged_walk_start(const PagedParams& p, PagedWalk
     if (w.bad && cta == 0) atomicExch(p.status, kDevBadIndex);
     total += __shfl_sync(0xffffffffu, upto, 31);
   }
-  k.per = max(quotient(total + n_ctas - 1, n_ctas), static_cast<long long>(p.min_steps));
+  k.per = (max(quotient(total + n_ctas - 1, n_ctas), static_cast<long long>(p.min_steps)) + 1) & ~1ll;
   k.at = min(k.per * cta, total);
   k.end = min(k.at + k.per, total);
-  k.b = k.head = k.u = k.blk = 0;
+  k.b = k.head = k.u = k.step = 0;
   if (k.at >= k.end) return;
   long long before = 0;  // steps of the sequences before b0
   int b0 = 0;
@@ -189,7 +198,7 @@ __device__ __forceinline__ void paged_walk_start(const PagedParams& p, PagedWalk
     }
     const int lu = in == 0 ? 0 : __ffs(in) - 1;
     k.u = u0 + lu;
-    k.blk = static_cast<int>(r - (__shfl_sync(0xffffffffu, sum, lu) - __shfl_sync(0xffffffffu, steps, lu)));
+    k.step = static_cast<int>(r - (__shfl_sync(0xffffffffu, sum, lu) - __shfl_sync(0xffffffffu, steps, lu)));
     break;
   }
 }
@@ -201,7 +210,9 @@ __device__ __forceinline__ PagedItem paged_walk_next(const PagedParams& p, Paged
   it.slot = -1;
   if (k.at >= k.end) return it;
   const int steps = unit_steps(p, k.w, k.u);
-  const int take = static_cast<int>(min(static_cast<long long>(steps - k.blk), k.end - k.at));
+  const int take = static_cast<int>(min(static_cast<long long>(steps - k.step), k.end - k.at));
+  it.dual = one_tile(p, k.w, k.u);
+  const int scale = it.dual ? 0 : 1;  // log2 of the steps of a block
   const int q0 = k.u * p.unit_pos;
   it.row0 = k.w.qs + q0;
   it.n_pos = min(p.unit_pos, k.w.n_new - q0);
@@ -209,10 +220,9 @@ __device__ __forceinline__ PagedItem paged_walk_next(const PagedParams& p, Paged
   it.len = k.w.len;
   it.head = k.head;
   it.seq = k.b;
-  it.j0 = k.blk;
-  const int j1 = k.blk + take;
+  it.j0 = k.step >> scale;
+  const int j1 = (k.step + take) >> scale;
   const int all = min(blocks_to(p, k.w, q0 + p.unit_pos), j1);
-  it.dual = it.n_pos <= p.tile_pos;
   if (it.dual) {
     const int n = max(all - it.j0, 0);
     it.nb0 = (n + 1) / 2;
@@ -223,12 +233,12 @@ __device__ __forceinline__ PagedItem paged_walk_next(const PagedParams& p, Paged
     it.nb1 = max(all - it.j0, 0);
     it.n_loads = max(it.nb0, it.nb1);
   }
-  if (take < steps) it.slot = 2 * cta + (k.blk == 0 ? 1 : 0);
+  if (take < steps) it.slot = 2 * cta + (k.step == 0 ? 1 : 0);
   // advance
   k.at += take;
-  k.blk += take;
-  if (k.blk == steps) {
-    k.blk = 0;
+  k.step += take;
+  if (k.step == steps) {
+    k.step = 0;
     if (++k.u == k.w.units) {
       k.u = 0;
       if (++k.head == p.H_kv) {
@@ -249,8 +259,8 @@ __device__ __forceinline__ PagedItem paged_walk_next(const PagedParams& p, Paged
 // last CTA, or row0 = -1 where the stretch starts a unit, is empty, or is not
 // the first one to start inside the unit (an earlier one merges it).
 __device__ __forceinline__ int4 paged_cut(const PagedParams& p, const PagedWalk& k, int cta) {
-  if (k.at >= k.end || k.blk == 0) return make_int4(-1, 0, 0, 0);
-  const long long start = k.at - k.blk;
+  if (k.at >= k.end || k.step == 0) return make_int4(-1, 0, 0, 0);
+  const long long start = k.at - k.step;
   if (start < (cta - 1) * k.per) return make_int4(-1, 0, 0, 0);
   const int q0 = k.u * p.unit_pos;
   const long long last = quotient(start + unit_steps(p, k.w, k.u) - 1, k.per);
@@ -260,57 +270,82 @@ __device__ __forceinline__ int4 paged_cut(const PagedParams& p, const PagedWalk&
 // Joins the pieces of the units that were cut.  Block (c, y): rows 8 y .. 8 y + 7 of the unit
 // that stretch c + 1 starts inside of: pieces 2 c + 1 and 2 c', c' = c + 1 .. last.
 //   lse = log2 sum_s 2^(lse_s),   O = sum_s 2^(lse_s - lse) O_s
-// It is a chain of reads (the record, then the pieces), so a piece's rows and log-sum-exps are asked for together:
-// up to 8 pieces by one warp per row; more (a long sequence over many CTAs) by the eight warps in turn, eight
-// at a time each, row by row.  The order of the sums depends on the lengths only.
-template <int D>
-struct MergeRow {
+// It is a chain of reads (the record, then the pieces), so their latency counts: a warp asks for the pieces of
+// its ROWS rows, four at a time each, together (four rows a warp for the chunk kernel's 256-row units: one row
+// a warp took 30 us for 147 cut units, in eight waves of blocks).  More than eight pieces (a long sequence over
+// many CTAs) are shared out among the block's eight warps, row by row.  The order of the sums depends on the
+// lengths only.
+template <int D, int ROWS>
+struct MergeRows {
   static constexpr int PER = D / 32;
-  float m = -INFINITY, sum = 0.f;
-  float acc[PER] = {};
+  using Vec = typename std::conditional<PER == 4, float4, float2>::type;
+  float m[ROWS], sum[ROWS], acc[ROWS][PER];
 
-  // adds pieces first, first + step, ... below n (at most eight of them)
+  __device__ __forceinline__ MergeRows() {
+#pragma unroll
+    for (int i = 0; i < ROWS; ++i) {
+      m[i] = -INFINITY;
+      sum[i] = 0.f;
+#pragma unroll
+      for (int x = 0; x < PER; ++x) acc[i][x] = 0.f;
+    }
+  }
+
+  // adds pieces first, first + step, ... below n (at most four of them) of rows r, r + 1, ...
   template <typename Place>
   __device__ __forceinline__ void add(const PagedParams& p, int r, int lane, int first, int step, int n, Place place) {
-    float l[8];
-    float2 v[8][PER / 2];
+    float l[ROWS][4];
+    Vec v[ROWS][4];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int s = first + i * step;
-      l[i] = -INFINITY;
-      if (s < n) {
-        const size_t at = static_cast<size_t>(place(s)) * p.unit_rows + r;
-        l[i] = p.l_part[at];
+    for (int i = 0; i < ROWS; ++i) {
 #pragma unroll
-        for (int x = 0; x < PER / 2; ++x) v[i][x] = reinterpret_cast<const float2*>(p.o_part + at * D + lane * PER)[x];
+      for (int j = 0; j < 4; ++j) {
+        const int s = first + j * step;
+        l[i][j] = -INFINITY;
+        if (s < n) {
+          const size_t at = static_cast<size_t>(place(s)) * p.unit_rows + r + i;
+          l[i][j] = p.l_part[at];
+          v[i][j] = *reinterpret_cast<const Vec*>(p.o_part + at * D + lane * PER);
+        }
       }
     }
-    float top = m;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) top = fmaxf(top, l[i]);
-    if (top == -INFINITY) return;  // no piece so far saw a key
-    const float old = m == -INFINITY ? 0.f : exp2_mufu(m - top);
-    sum *= old;
+    for (int i = 0; i < ROWS; ++i) {
+      const float top = fmaxf(fmaxf(fmaxf(l[i][0], l[i][1]), fmaxf(l[i][2], l[i][3])), m[i]);
+      if (top == -INFINITY) continue;  // no piece so far saw a key
+      const float old = m[i] == -INFINITY ? 0.f : exp2_mufu(m[i] - top);
+      sum[i] *= old;
 #pragma unroll
-    for (int x = 0; x < PER; ++x) acc[x] *= old;
+      for (int x = 0; x < PER; ++x) acc[i][x] *= old;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      if (l[i] == -INFINITY) continue;
-      const float w = exp2_mufu(l[i] - top);
-      sum += w;
+      for (int j = 0; j < 4; ++j) {
+        if (l[i][j] == -INFINITY) continue;
+        const float w = exp2_mufu(l[i][j] - top);
+        sum[i] += w;
 #pragma unroll
-      for (int x = 0; x < PER / 2; ++x) {
-        acc[2 * x] += w * v[i][x].x;
-        acc[2 * x + 1] += w * v[i][x].y;
+        for (int x = 0; x < PER; ++x) acc[i][x] += w * reinterpret_cast<const float*>(&v[i][j])[x];
       }
+      m[i] = top;
     }
-    m = top;
   }
 };
 
+// Where row r of a unit is (tile rows are position-major): its token and head; false for padding.
+template <int TILE_ROWS>
+__device__ __forceinline__ bool unit_row(const PagedParams& p, int r, int n_pos, int& pos, int& head) {
+  const int rr = r % TILE_ROWS;
+  pos = rr / p.group;
+  head = rr - pos * p.group;
+  const bool real = pos < p.tile_pos;
+  pos += r / TILE_ROWS * p.tile_pos;
+  return real && pos < n_pos;
+}
+
+__host__ __device__ constexpr int merge_rows(int tile_rows) { return tile_rows == 128 ? 4 : 1; }  // rows of a warp
+
 template <int D, int TILE_ROWS>
 __global__ void __launch_bounds__(256) paged_merge_kernel(const PagedParams p) {
-  constexpr int PER = D / 32;
+  constexpr int PER = D / 32, ROWS = merge_rows(TILE_ROWS);
   __shared__ __align__(16) float red_o[8][D];
   __shared__ float red_m[8], red_l[8];
   // a programmatic dependent of the attention kernel: waits for its results
@@ -322,54 +357,62 @@ __global__ void __launch_bounds__(256) paged_merge_kernel(const PagedParams p) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int n = cut.w - c + 2;  // pieces
   auto place = [&](int s) { return s == 0 ? 2 * c - 1 : 2 * (c + s - 1); };
-  const bool wide = n > 8;
-  for (int i = 0; i < (wide ? 8 : 1); ++i) {
-    const int r = blockIdx.y * 8 + (wide ? i : warp);
-    if (r >= p.unit_rows) break;
-    const int rr = r % TILE_ROWS;
-    const int pos = r / TILE_ROWS * p.tile_pos + rr / p.group;
-    const bool valid = rr < p.group * p.tile_pos && pos < cut.y;
-    if (!valid) continue;  // (the same for the whole block when wide)
-    MergeRow<D> row;
-    if (!wide) {
-      row.add(p, r, lane, 0, 1, n, place);
-    } else {
-      for (int s = warp; s < n; s += 64) row.add(p, r, lane, s, 8, n, place);
-#pragma unroll
-      for (int x = 0; x < PER; ++x) red_o[warp][lane * PER + x] = row.acc[x];
-      if (lane == 0) {
-        red_m[warp] = row.m;
-        red_l[warp] = row.sum;
-      }
-      __syncthreads();
-      if (warp == 0) {
-        float top = red_m[0];
-#pragma unroll
-        for (int g = 1; g < 8; ++g) top = fmaxf(top, red_m[g]);
-        row = MergeRow<D>{};
-        row.m = top;
-        if (top > -INFINITY) {
-#pragma unroll
-          for (int g = 0; g < 8; ++g) {
-            const float w = exp2_mufu(red_m[g] - top);
-            row.sum += w * red_l[g];
-#pragma unroll
-            for (int x = 0; x < PER; ++x) row.acc[x] += w * red_o[g][lane * PER + x];
-          }
-        }
-      }
-      __syncthreads();
-      if (warp != 0) continue;
-    }
-    const float inv = row.sum > 0.f ? 1.f / row.sum : 0.f;
-    const int h = cut.z * p.group + rr % p.group;
+  auto finish = [&](int r, float m, float sum, const float* acc) {
+    int pos, head;
+    if (!unit_row<TILE_ROWS>(p, r, cut.y, pos, head)) return;
+    const float inv = sum > 0.f ? 1.f / sum : 0.f;
+    const int h = cut.z * p.group + head;
     const long long at = static_cast<long long>(cut.x) + pos;
     uint32_t* dst = reinterpret_cast<uint32_t*>(p.o + (at * p.H_q + h) * D + lane * PER);
 #pragma unroll
-    for (int x = 0; x < PER / 2; ++x) dst[x] = pack_bf16x2(row.acc[2 * x] * inv, row.acc[2 * x + 1] * inv);
+    for (int x = 0; x < PER / 2; ++x) dst[x] = pack_bf16x2(acc[2 * x] * inv, acc[2 * x + 1] * inv);
     if (lane == 0)
-      p.lse[static_cast<long long>(h) * p.n_tokens + at] =
-          row.sum > 0.f ? (row.m + log2f(row.sum)) * 0.69314718055994531f : -INFINITY;
+      p.lse[static_cast<long long>(h) * p.n_tokens + at] = sum > 0.f ? (m + log2f(sum)) * 0.69314718055994531f : -INFINITY;
+  };
+  const int r0 = blockIdx.y * 8 * ROWS;
+  int pos, head;
+  if (n <= 8) {
+    const int r = r0 + warp * ROWS;
+    bool any = false;  // (padding rows hold no partial result: they are read, and dropped)
+#pragma unroll
+    for (int i = 0; i < ROWS; ++i) any |= unit_row<TILE_ROWS>(p, r + i, cut.y, pos, head);
+    if (!any) return;
+    MergeRows<D, ROWS> rows;
+    rows.add(p, r, lane, 0, 1, n, place);
+    if (n > 4) rows.add(p, r, lane, 4, 1, n, place);
+#pragma unroll
+    for (int i = 0; i < ROWS; ++i) finish(r + i, rows.m[i], rows.sum[i], rows.acc[i]);
+    return;
+  }
+  for (int r = r0; r < r0 + 8 * ROWS; ++r) {
+    if (!unit_row<TILE_ROWS>(p, r, cut.y, pos, head)) continue;  // (the same for the whole block)
+    MergeRows<D, 1> row;
+    for (int s = warp; s < n; s += 32) row.add(p, r, lane, s, 8, n, place);
+#pragma unroll
+    for (int x = 0; x < PER; ++x) red_o[warp][lane * PER + x] = row.acc[0][x];
+    if (lane == 0) {
+      red_m[warp] = row.m[0];
+      red_l[warp] = row.sum[0];
+    }
+    __syncthreads();
+    if (warp == 0) {
+      float top = red_m[0], sum = 0.f, acc[PER];
+#pragma unroll
+      for (int g = 1; g < 8; ++g) top = fmaxf(top, red_m[g]);
+#pragma unroll
+      for (int x = 0; x < PER; ++x) acc[x] = 0.f;
+      if (top > -INFINITY) {
+#pragma unroll
+        for (int g = 0; g < 8; ++g) {
+          const float w = exp2_mufu(red_m[g] - top);
+          sum += w * red_l[g];
+#pragma unroll
+          for (int x = 0; x < PER; ++x) acc[x] += w * red_o[g][lane * PER + x];
+        }
+      }
+      finish(r, top, sum, acc);
+    }
+    __syncthreads();
   }
 }
 
