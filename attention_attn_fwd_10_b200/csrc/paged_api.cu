@@ -208,6 +208,7 @@ cudaError_t launch_paged(void (*kern)(CUtensorMap, CUtensorMap, CUtensorMap, Pag
   p.tile_pos = TILE_ROWS / p.group;
   p.unit_pos = tiles * p.tile_pos;
   p.unit_rows = tiles * TILE_ROWS;
+  p.unit_extra = tiles == 2 ? 2 : 0;
   p.min_steps = 2;  // a 2000-key decoding call took 16.8, 12.5, 14.2, 20.3 us with 1, 2, 4, 8
   const PagedWorkspace w = paged_workspace(p.unit_rows, D);
   uint8_t* ws = static_cast<uint8_t*>(workspace);

@@ -37,6 +37,7 @@ struct PagedParams {
   int causal;
   int tile_pos, unit_pos;      // tokens of a tile, of a unit
   int unit_rows;               // rows of a unit's partial result
+  int unit_extra;              // steps that stand for a unit's start and end (even)
   int min_steps;               // least steps of a CTA's stretch
   float* o_part;               // [2 gridDim.x, unit_rows, D]
   float* l_part;               // [2 gridDim.x, unit_rows], base-2 log-sum-exp
@@ -89,7 +90,7 @@ __device__ __forceinline__ bool one_tile(const PagedParams& p, const SeqWork& w,
 }
 __device__ __forceinline__ int unit_steps(const PagedParams& p, const SeqWork& w, int u) {
   const int blocks = max(1, blocks_to(p, w, (u + 1) * p.unit_pos));
-  return one_tile(p, w, u) ? (blocks + 1) & ~1 : 2 * blocks;
+  return (one_tile(p, w, u) ? (blocks + 1) & ~1 : 2 * blocks) + p.unit_extra;
 }
 
 __device__ __forceinline__ long long warp_sum(long long x) {
