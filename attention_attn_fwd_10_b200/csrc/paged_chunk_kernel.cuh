@@ -53,7 +53,7 @@ struct ChunkLayout {
   static constexpr int VST = KV8 ? (D == 128 ? 2 : 4) : (D == 128 ? 2 : 4);
   // V as the MMA reads it: D / 64 columns of 128-byte rows of 16-bit values (e4m3: written by the converters)
   static constexpr int VM_BYTES = 128 * D * 2;
-  static constexpr int VMST = KV8 ? 2 : VST;
+  static constexpr int VMST = KV8 ? (D == 64 ? 4 : 2) : VST;
   static constexpr int Q_OFF = 0;
   static constexpr int K_OFF = 2 * Q_BYTES;
   static constexpr int V_OFF = K_OFF + KST * KV_BYTES;   // as loaded
@@ -253,7 +253,7 @@ __global__ void __launch_bounds__(ChunkLayout<D, KV8>::THREADS, 1)
           ++qn;
         }
       }
-      PageWindow win{-1, -1};
+      PageWindow win{-1, -1, 0};
       for (int j = 0; ok && j < n_loads; ++j) {
         const int s = kn % L::KST;
         if (kn >= L::KST && !(ok = __all_sync(0xffffffffu, mbar_wait(bar(L::B_K_EMPTY + s), ((kn / L::KST) - 1) & 1, ctl))))
@@ -280,7 +280,7 @@ __global__ void __launch_bounds__(ChunkLayout<D, KV8>::THREADS, 1)
       const int row0 = it->row0, head = it->head, seq = it->seq, len = it->len, j0 = it->j0, n_loads = it->n_loads;
       mbar_arrive_warp(item_done(u));
       if (row0 < 0) break;
-      PageWindow win{-1, -1};
+      PageWindow win{-1, -1, 0};
       for (int j = 0; ok && j < n_loads; ++j) {
         const int s = vn % L::VST;
         if (vn >= L::VST && !(ok = __all_sync(0xffffffffu, mbar_wait(bar(L::B_V_EMPTY + s), ((vn / L::VST) - 1) & 1, ctl))))

@@ -12,10 +12,10 @@
 // thread until the piece ends.  Warps:
 //   0-3, 4-7  softmax of the even and the odd blocks (two streams with statistics and
 //             accumulator of their own, joined at the piece's end by the first)
-//   8         TMA producer of Q (bf16 cache), K and V
+//   8         TMA producer of Q (bf16 cache) and K
 //   9         tensor memory; issues the S MMAs, up to four blocks ahead of P V, across pieces
 //   10        issues the P V MMAs (and writes zeros over V's rows past a sequence's end)
-//   11        scheduler; e4m3 cache: also writes Q as two e4m3 terms
+//   11        scheduler and TMA producer of V; e4m3 cache: also writes Q as two e4m3 terms
 // P^T goes to shared memory (the B operand's place), four buffers in turn.
 //
 // An MMA of M = 128 and N <= 32 takes 46 clk whatever N is (65 at N = 128), and issuing one about as long: with
@@ -68,7 +68,7 @@ struct FewLayout {
   static constexpr int B_ITEM_EMPTY = B_ITEM_FULL + NI;
   static constexpr int B_DRAIN = B_ITEM_EMPTY + NI;
   static constexpr int N_BARS = B_DRAIN + 2;
-  static constexpr int ITEM_READERS = 11;  // 8 softmax warps, the producer, the two issuers
+  static constexpr int ITEM_READERS = 11;  // 8 softmax warps, K's producer, the two issuers
   static constexpr int ITEM_OFF = BAR_OFF + (8 * N_BARS + 15) / 16 * 16;
   static constexpr int CQ_OFF = ITEM_OFF + NI * static_cast<int>(sizeof(PagedItem));  // [NI][NQ] factors of the scores
   static constexpr int STAT_OFF = CQ_OFF + NI * NQ * 4;    // [2 streams][5][NQ]: four warps' sums, the maximum
@@ -86,7 +86,7 @@ struct FewLayout {
   __device__ static constexpr uint32_t o_col(int t) { return static_cast<uint32_t>(NBUF + t) * NS; }
   static constexpr uint32_t TMEM_COLS = NS == 16 ? 128 : (NS == 32 ? 256 : 512);
   static constexpr int THREADS = 384;
-  static constexpr int WARP_LOAD = 8, WARP_S = 9, WARP_PV = 10, WARP_SCHED = 11;
+  static constexpr int WARP_K = 8, WARP_S = 9, WARP_PV = 10, WARP_SCHED = 11;
   // weights up to 2^(SHIFT + TAU) = 2^8; a column's largest at 2^SHIFT or more
   static constexpr float SHIFT = KV8 ? 3.f : 0.f;
   static constexpr float TAU = KV8 ? 5.f : 8.f;
@@ -197,7 +197,7 @@ __global__ void __launch_bounds__(FewLayout<D, KV8, NQ>::THREADS, 1)
     tmem_alloc(sbase + L::TMEM_SLOT_OFF, L::TMEM_COLS);
     tmem_relinquish();
   }
-  if (warp == L::WARP_LOAD && lane == 0) {
+  if (warp == L::WARP_K && lane == 0) {
     if (!KV8) tma_prefetch_desc(&tm_q);
     tma_prefetch_desc(&tm_k);
     tma_prefetch_desc(&tm_v);
@@ -224,8 +224,8 @@ __global__ void __launch_bounds__(FewLayout<D, KV8, NQ>::THREADS, 1)
   auto wait_item = [&](int u) { return mbar_wait(bar(L::B_ITEM_FULL + u % L::NI), (u / L::NI) & 1, ctl); };
   auto item_done = [&](int u) { return bar(L::B_ITEM_EMPTY + u % L::NI); };
 
-  if (warp == L::WARP_LOAD) {
-    // ===================== TMA producer: Q, K, V =====================
+  if (warp == L::WARP_K) {
+    // ===================== TMA producer: Q, K =====================
     int kn = 0, qn = 0;
     bool ok = true;
     for (int u = 0; ok; ++u) {
@@ -247,18 +247,12 @@ __global__ void __launch_bounds__(FewLayout<D, KV8, NQ>::THREADS, 1)
         }
         ++qn;
       }
-      PageWindow win{-1, -1};
+      PageWindow win{-1, -1, 0};
       for (int j = 0; ok && j < n_loads; ++j, ++kn) {
         const int s = kn % L::ST;
-        const uint32_t ph = ((kn / L::ST) - 1) & 1;
-        if (kn >= L::ST && !(ok = __all_sync(0xffffffffu, mbar_wait(bar(L::B_K_EMPTY + s), ph, ctl)))) break;
-        load_block<L::NBOX, L::ROW_BYTES>(p, &tm_k, sbase + L::K_OFF + s * L::KV_BYTES, bar(L::B_K_FULL + s), win, seq, head,
-                                          len, j0 + j, lane);
-        if (kn >= L::ST && !(ok = __all_sync(0xffffffffu, mbar_wait(bar(L::B_V_EMPTY + s), ph, ctl)))) {
-          mbar_wait_drain(bar(L::B_K_FULL + s), (kn / L::ST) & 1, 1000000000ull);  // its V was not asked for
+        if (kn >= L::ST && !(ok = __all_sync(0xffffffffu, mbar_wait(bar(L::B_K_EMPTY + s), ((kn / L::ST) - 1) & 1, ctl))))
           break;
-        }
-        load_block<L::NBOX, L::ROW_BYTES>(p, &tm_v, sbase + L::V_OFF + s * L::KV_BYTES, bar(L::B_V_FULL + s), win, seq, head,
+        load_block<L::NBOX, L::ROW_BYTES>(p, &tm_k, sbase + L::K_OFF + s * L::KV_BYTES, bar(L::B_K_FULL + s), win, seq, head,
                                           len, j0 + j, lane);
       }
     }
@@ -268,7 +262,6 @@ __global__ void __launch_bounds__(FewLayout<D, KV8, NQ>::THREADS, 1)
     for (int i = 0; i < L::ST && i < kn; ++i) {
       const int n = kn - 1 - i;
       mbar_wait_drain(bar(L::B_K_FULL + n % L::ST), (n / L::ST) & 1, 1000000000ull);
-      mbar_wait_drain(bar(L::B_V_FULL + n % L::ST), (n / L::ST) & 1, 1000000000ull);
     }
   } else if (warp == L::WARP_S) {
     // ===================== S^T = K Q^T =====================
@@ -364,10 +357,11 @@ __global__ void __launch_bounds__(FewLayout<D, KV8, NQ>::THREADS, 1)
       mbar_wait_drain(bar(L::B_DRAIN + 1), 0, 1000000000ull);
     }
   } else if (warp == L::WARP_SCHED) {
-    // ===================== scheduler =====================
+    // ===================== scheduler; TMA producer: V =====================
     if (lane == 0) p.cut[cta] = paged_cut(p, walk, cta);
-    int qn = 0;
-    for (int u = 0;; ++u) {
+    int qn = 0, vn = 0;
+    bool ok = true;
+    for (int u = 0; ok; ++u) {
       const PagedItem it = paged_walk_next(p, walk, cta);
       if (u >= L::NI && !__all_sync(0xffffffffu, mbar_wait(item_done(u), ((u / L::NI) - 1) & 1, ctl))) break;
       const bool q_here = KV8 && it.row0 >= 0 && it.n_loads > 0;
@@ -405,7 +399,18 @@ __global__ void __launch_bounds__(FewLayout<D, KV8, NQ>::THREADS, 1)
         mbar_arrive(bar(L::B_ITEM_FULL + u % L::NI));
       }
       if (it.row0 < 0) break;
+      PageWindow win{-1, -1, 0};
+      int j = 0;
+      auto load_v = [&] {
+        const int s = vn % L::ST;
+        if (vn >= L::ST && !(ok = __all_sync(0xffffffffu, mbar_wait(bar(L::B_V_EMPTY + s), ((vn / L::ST) - 1) & 1, ctl))))
+          return;
+        load_block<L::NBOX, L::ROW_BYTES>(p, &tm_v, sbase + L::V_OFF + s * L::KV_BYTES, bar(L::B_V_FULL + s), win, it.seq,
+                                          it.head, it.len, it.j0 + j, lane);
+        ++vn;
+      };
       if (q_here) {
+        for (; j < it.n_loads && vn < L::ST; ++j) load_v();  // (the first blocks, while the ring is empty)
         const int qs = qn & 1;
         if (qn >= 2 && !__all_sync(0xffffffffu, mbar_wait(bar(L::B_Q_EMPTY + qs), ((qn >> 1) - 1) & 1, ctl))) break;
         if (lane < NQ) {
@@ -435,6 +440,11 @@ __global__ void __launch_bounds__(FewLayout<D, KV8, NQ>::THREADS, 1)
         if (lane == 0) mbar_arrive(bar(L::B_Q_FULL + qs));
         ++qn;
       }
+      for (; ok && j < it.n_loads; ++j) load_v();
+    }
+    for (int i = 0; i < L::ST && i < vn; ++i) {
+      const int n = vn - 1 - i;
+      mbar_wait_drain(bar(L::B_V_FULL + n % L::ST), (n / L::ST) & 1, 1000000000ull);
     }
   } else {
     // ===================== softmax warpgroups =====================

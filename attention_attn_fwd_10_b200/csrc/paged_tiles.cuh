@@ -42,7 +42,7 @@ __device__ __forceinline__ float q_factor(float scale_log2, uint32_t power) {
 // A producer warp's page numbers: lane l holds the page of box base + l of the current sequence.
 struct PageWindow {
   int base;  // first box held; -1: none
-  int page;
+  int page, slot;  // the lane's box: its page, its first slot there
 };
 
 // The page of box `box` of sequence `seq` (all lanes call with their own box, within one window of 32 boxes that
@@ -50,9 +50,12 @@ struct PageWindow {
 __device__ __forceinline__ void window_load(const PagedParams& p, PageWindow& w, int seq, int base, int n_boxes, int lane) {
   w.base = base;
   w.page = -1;
+  w.slot = 0;
   const int box = base + lane;
   if (box < n_boxes) {
-    const int page = p.page_table[seq * p.table_stride + (box << p.box_shift) / p.page_size];
+    const int j = (box << p.box_shift) / p.page_size;
+    w.slot = (box << p.box_shift) - j * p.page_size;
+    const int page = p.page_table[seq * p.table_stride + j];
     if (page >= 0 && page < p.n_pages)
       w.page = page;
     else
@@ -62,7 +65,9 @@ __device__ __forceinline__ void window_load(const PagedParams& p, PageWindow& w,
 
 // Loads block `blk` (128 keys) of a sequence's cache into shared memory at `dst`: box i of the block by lane i of
 // the warp (lane i + boxes: its second 128-byte column); `full` completes when all of them have landed.
-// NBOX columns of ROW_BYTES; boxes wholly past the sequence's end are left out.
+// NBOX columns of ROW_BYTES; boxes wholly past the sequence's end are left out.  A warp issues a TMA instruction
+// in about 100 clk (lane by lane or in a loop of one lane alike), so pages of 16 keys, 16 boxes a tile, take 1.6k
+// clk a tile: K and V have a warp each.
 template <int NBOX, int ROW_BYTES>
 __device__ __forceinline__ void load_block(const PagedParams& p, const CUtensorMap* map, uint32_t dst, uint32_t full,
                                            PageWindow& win, int seq, int head, int len, int blk, int lane) {
@@ -75,9 +80,9 @@ __device__ __forceinline__ void load_block(const PagedParams& p, const CUtensorM
   __syncwarp();
   const int i = lane & ((1 << boxes_log2) - 1), x = lane >> boxes_log2;
   const int page = __shfl_sync(0xffffffffu, win.page, (first + i) & 31);
+  const int slot = __shfl_sync(0xffffffffu, win.slot, (first + i) & 31);
   if (i < n && x < NBOX)
-    tma_load_4d(dst + x * 128 * ROW_BYTES + i * p.box_rows * ROW_BYTES, map, full, x * 64, head,
-                ((first + i) << p.box_shift) % p.page_size, page);
+    tma_load_4d(dst + x * 128 * ROW_BYTES + i * p.box_rows * ROW_BYTES, map, full, x * 64, head, slot, page);
 }
 
 // Writes zeros over the rows of a landed block that lie past the sequence's end (`live` keys are the sequence's), by
