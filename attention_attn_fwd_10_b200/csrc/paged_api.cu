@@ -208,8 +208,9 @@ cudaError_t launch_paged(void (*kern)(CUtensorMap, CUtensorMap, CUtensorMap, Pag
   p.tile_pos = TILE_ROWS / p.group;
   p.unit_pos = tiles * p.tile_pos;
   p.unit_rows = tiles * TILE_ROWS;
-  p.unit_extra = tiles == 2 ? 2 : 0;
-  p.min_steps = 2;  // a 2000-key decoding call took 16.8, 12.5, 14.2, 20.3 us with 1, 2, 4, 8
+  p.step_log2 = tiles - 1;
+  p.unit_extra = tiles == 2 ? 2 : 4;
+  p.min_steps = 2;
   const PagedWorkspace w = paged_workspace(p.unit_rows, D);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   p.cut = reinterpret_cast<int4*>(ws);
@@ -370,7 +371,7 @@ attn_status_t attn_fwd_paged(const attn_paged_kv_t* c, const void* q, void* o, f
   p.q_stride = q_stride;
   p.n_pages = c->n_pages;
   p.page_size = c->page_size;
-  p.max_pages = c->max_pages;
+  p.room = c->max_pages * c->page_size;
   p.n_seq = c->n_seq;
   while (p.box_shift < 7 && c->page_size % (2 << p.box_shift) == 0) ++p.box_shift;
   p.box_rows = 1 << p.box_shift;

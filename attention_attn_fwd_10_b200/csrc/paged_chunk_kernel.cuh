@@ -164,7 +164,7 @@ __device__ __forceinline__ float exp_half_f16(const uint32_t* sr, float c, float
 template <int D, bool KV8>
 __global__ void __launch_bounds__(ChunkLayout<D, KV8>::THREADS, 1)
     paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
-                       const __grid_constant__ CUtensorMap tm_v, const PagedParams p) {
+                       const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ PagedParams p) {
   using L = ChunkLayout<D, KV8>;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);

@@ -12,10 +12,10 @@
 // thread until the piece ends.  Warps:
 //   0-3, 4-7  softmax of the even and the odd blocks (two streams with statistics and
 //             accumulator of their own, joined at the piece's end by the first)
-//   8         TMA producer of Q (bf16 cache) and K
+//   8         TMA producer of Q (bf16 cache), of K, and of V where a block is few boxes
 //   9         tensor memory; issues the S MMAs, up to four blocks ahead of P V, across pieces
 //   10        issues the P V MMAs (and writes zeros over V's rows past a sequence's end)
-//   11        scheduler and TMA producer of V; e4m3 cache: also writes Q as two e4m3 terms
+//   11        scheduler; e4m3 cache: writes Q as two e4m3 terms; pages of less than 64 keys: TMA producer of V
 // P^T goes to shared memory (the B operand's place), four buffers in turn.
 //
 // An MMA of M = 128 and N <= 32 takes 46 clk whatever N is (65 at N = 128), and issuing one about as long: with
@@ -52,8 +52,8 @@ struct FewLayout {
   static constexpr int Q_OFF = P_OFF + NBUF * P_BYTES;
   static constexpr int BAR_OFF = Q_OFF + 2 * Q_BYTES;
   static constexpr int NI = 4;
-  static constexpr int B_Q_FULL = 0;                    // [2]
-  static constexpr int B_Q_EMPTY = B_Q_FULL + 2;        // [2]
+  static constexpr int B_Q_FULL = 0;                    // [NI] by piece: its Q, and the factors of its scores
+  static constexpr int B_Q_EMPTY = B_Q_FULL + NI;       // [2] by Q tile
   static constexpr int B_K_FULL = B_Q_EMPTY + 2;        // [ST]
   static constexpr int B_K_EMPTY = B_K_FULL + ST;
   static constexpr int B_V_FULL = B_K_EMPTY + ST;
@@ -168,7 +168,7 @@ __device__ __forceinline__ float warp_columns(const float* x, int lane, Op op) {
 template <int D, bool KV8, int NQ>
 __global__ void __launch_bounds__(FewLayout<D, KV8, NQ>::THREADS, 1)
     paged_few_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
-                     const __grid_constant__ CUtensorMap tm_v, const PagedParams p) {
+                     const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ PagedParams p) {
   using L = FewLayout<D, KV8, NQ>;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
@@ -223,10 +223,14 @@ __global__ void __launch_bounds__(FewLayout<D, KV8, NQ>::THREADS, 1)
   };
   auto wait_item = [&](int u) { return mbar_wait(bar(L::B_ITEM_FULL + u % L::NI), (u / L::NI) & 1, ctl); };
   auto item_done = [&](int u) { return bar(L::B_ITEM_EMPTY + u % L::NI); };
+  // One warp loads K and V in turn, unless a tile is many boxes (a warp issues one in about 100 clk): 4 x 32768 e4m3
+  // keys in pages of 128 took 59 us with one warp and 63 with two, 64 sequences in pages of 16 211 and 176.
+  const bool one_loader = p.box_shift >= 6;
 
   if (warp == L::WARP_K) {
     // ===================== TMA producer: Q, K =====================
-    int kn = 0, qn = 0;
+    int kn = 0, vn = 0, qn = 0;
+    int last_q[2] = {0, 0};  // the last pieces whose Q this warp loaded
     bool ok = true;
     for (int u = 0; ok; ++u) {
       if (!(ok = __all_sync(0xffffffffu, wait_item(u)))) break;
@@ -234,34 +238,49 @@ __global__ void __launch_bounds__(FewLayout<D, KV8, NQ>::THREADS, 1)
       const int row0 = it->row0, head = it->head, seq = it->seq, len = it->len, j0 = it->j0, n_loads = it->n_loads;
       mbar_arrive_warp(item_done(u));
       if (row0 < 0) break;
-      if (n_loads == 0) continue;
+      if (n_loads == 0) {
+        if (!KV8 && lane == 0) mbar_arrive(bar(L::B_Q_FULL + u % L::NI));
+        continue;
+      }
       if constexpr (!KV8) {
         const int qs = qn & 1;
         if (qn >= 2 && !(ok = __all_sync(0xffffffffu, mbar_wait(bar(L::B_Q_EMPTY + qs), ((qn >> 1) - 1) & 1, ctl)))) break;
         if (lane == 0) {
-          mbar_arrive_expect_tx(bar(L::B_Q_FULL + qs), L::NBOX * p.group * p.tile_pos * 128);
+          mbar_arrive_expect_tx(bar(L::B_Q_FULL + u % L::NI), L::NBOX * p.group * p.tile_pos * 128);
 #pragma unroll
           for (int x = 0; x < L::NBOX; ++x)
-            tma_load_4d(sbase + L::Q_OFF + qs * L::Q_BYTES + x * L::Q_COL, &tm_q, bar(L::B_Q_FULL + qs), x * 64,
+            tma_load_4d(sbase + L::Q_OFF + qs * L::Q_BYTES + x * L::Q_COL, &tm_q, bar(L::B_Q_FULL + u % L::NI), x * 64,
                         head * p.group, row0, 0);
         }
+        last_q[1] = last_q[0];
+        last_q[0] = u;
         ++qn;
       }
       PageWindow win{-1, -1, 0};
-      for (int j = 0; ok && j < n_loads; ++j, ++kn) {
+      for (int j = 0; ok && j < n_loads; ++j) {
         const int s = kn % L::ST;
-        if (kn >= L::ST && !(ok = __all_sync(0xffffffffu, mbar_wait(bar(L::B_K_EMPTY + s), ((kn / L::ST) - 1) & 1, ctl))))
-          break;
+        const uint32_t ph = ((kn / L::ST) - 1) & 1;
+        if (kn >= L::ST && !(ok = __all_sync(0xffffffffu, mbar_wait(bar(L::B_K_EMPTY + s), ph, ctl)))) break;
         load_block<L::NBOX, L::ROW_BYTES>(p, &tm_k, sbase + L::K_OFF + s * L::KV_BYTES, bar(L::B_K_FULL + s), win, seq, head,
                                           len, j0 + j, lane);
+        ++kn;
+        if (!one_loader) continue;
+        if (vn >= L::ST && !(ok = __all_sync(0xffffffffu, mbar_wait(bar(L::B_V_EMPTY + s), ph, ctl)))) break;
+        load_block<L::NBOX, L::ROW_BYTES>(p, &tm_v, sbase + L::V_OFF + s * L::KV_BYTES, bar(L::B_V_FULL + s), win, seq, head,
+                                          len, j0 + j, lane);
+        ++vn;
       }
     }
     // Drain: every load this warp issued has landed before the CTA may exit.
     for (int i = 0; i < 2 && i < qn; ++i)
-      mbar_wait_drain(bar(L::B_Q_FULL + ((qn - 1 - i) & 1)), ((qn - 1 - i) >> 1) & 1, 1000000000ull);
+      mbar_wait_drain(bar(L::B_Q_FULL + last_q[i] % L::NI), (last_q[i] / L::NI) & 1, 1000000000ull);
     for (int i = 0; i < L::ST && i < kn; ++i) {
       const int n = kn - 1 - i;
       mbar_wait_drain(bar(L::B_K_FULL + n % L::ST), (n / L::ST) & 1, 1000000000ull);
+    }
+    for (int i = 0; i < L::ST && i < vn; ++i) {
+      const int n = vn - 1 - i;
+      mbar_wait_drain(bar(L::B_V_FULL + n % L::ST), (n / L::ST) & 1, 1000000000ull);
     }
   } else if (warp == L::WARP_S) {
     // ===================== S^T = K Q^T =====================
@@ -281,7 +300,7 @@ __global__ void __launch_bounds__(FewLayout<D, KV8, NQ>::THREADS, 1)
           // four blocks ago: the scores were read before P was published, and P V is complete, so the softmax
           // that S_FULL wakes finds its P buffer free
           if (ok && g >= L::NBUF) ok = mbar_wait(bar(L::B_PV_DONE + buf), ((g / L::NBUF) - 1) & 1, ctl);
-          if (ok && j == 0) ok = mbar_wait(bar(L::B_Q_FULL + (qi & 1)), (qi >> 1) & 1, ctl);
+          if (ok && j == 0) ok = mbar_wait(bar(L::B_Q_FULL + u % L::NI), (u / L::NI) & 1, ctl);
           if (!ok) break;
           tc_fence_after();
           const uint32_t kd = sdesc_lo(sbase + L::K_OFF + stage * L::KV_BYTES, 16);
@@ -357,40 +376,13 @@ __global__ void __launch_bounds__(FewLayout<D, KV8, NQ>::THREADS, 1)
       mbar_wait_drain(bar(L::B_DRAIN + 1), 0, 1000000000ull);
     }
   } else if (warp == L::WARP_SCHED) {
-    // ===================== scheduler; TMA producer: V =====================
+    // ===================== scheduler; small pages: TMA producer of V =====================
     if (lane == 0) p.cut[cta] = paged_cut(p, walk, cta);
     int qn = 0, vn = 0;
     bool ok = true;
     for (int u = 0; ok; ++u) {
       const PagedItem it = paged_walk_next(p, walk, cta);
       if (u >= L::NI && !__all_sync(0xffffffffu, mbar_wait(item_done(u), ((u / L::NI) - 1) & 1, ctl))) break;
-      const bool q_here = KV8 && it.row0 >= 0 && it.n_loads > 0;
-      const bool real = lane < p.group * it.n_pos;  // lane = column of the unit
-      uint4 w[KV8 ? D / 8 : 1];
-      uint32_t up = 0;
-      if (q_here) {
-        // the power of two that puts the row's largest element into [128, 256)
-#pragma unroll
-        for (int i = 0; i < (KV8 ? D / 8 : 1); ++i) w[i] = make_uint4(0, 0, 0, 0);
-        if (real) {
-          const int pos = lane / p.group;
-          const uint4* src = reinterpret_cast<const uint4*>(p.q + (static_cast<long long>(it.row0) + pos) * p.q_stride +
-                                                            static_cast<long long>(it.head * p.group + lane - pos * p.group) * D);
-#pragma unroll
-          for (int i = 0; i < (KV8 ? D / 8 : 1); ++i) w[i] = src[i];
-        }
-        uint32_t most = 0;
-#pragma unroll
-        for (int i = 0; i < (KV8 ? D / 8 : 1); ++i)
-          most = max(max(most, max(max(w[i].x & 0x7f80u, w[i].y & 0x7f80u), max(w[i].z & 0x7f80u, w[i].w & 0x7f80u))),
-                     max(max((w[i].x >> 16) & 0x7f80u, (w[i].y >> 16) & 0x7f80u),
-                         max((w[i].z >> 16) & 0x7f80u, (w[i].w >> 16) & 0x7f80u)));
-        up = q_power(most);
-        if (lane < NQ)
-          reinterpret_cast<float*>(sptr + L::CQ_OFF)[(u % L::NI) * NQ + lane] =
-              real ? q_factor(p.scale_log2, up) : 0.f;
-        __syncwarp();
-      }
       if (lane == 0) {
         volatile int* dst = reinterpret_cast<volatile int*>(sptr + L::ITEM_OFF + (u % L::NI) * sizeof(PagedItem));
         const int* from = reinterpret_cast<const int*>(&it);
@@ -400,7 +392,7 @@ __global__ void __launch_bounds__(FewLayout<D, KV8, NQ>::THREADS, 1)
       }
       if (it.row0 < 0) break;
       PageWindow win{-1, -1, 0};
-      int j = 0;
+      int j = one_loader ? it.n_loads : 0;
       auto load_v = [&] {
         const int s = vn % L::ST;
         if (vn >= L::ST && !(ok = __all_sync(0xffffffffu, mbar_wait(bar(L::B_V_EMPTY + s), ((vn / L::ST) - 1) & 1, ctl))))
@@ -409,19 +401,38 @@ __global__ void __launch_bounds__(FewLayout<D, KV8, NQ>::THREADS, 1)
                                           it.head, it.len, it.j0 + j, lane);
         ++vn;
       };
-      if (q_here) {
-        for (; j < it.n_loads && vn < L::ST; ++j) load_v();  // (the first blocks, while the ring is empty)
-        const int qs = qn & 1;
-        if (qn >= 2 && !__all_sync(0xffffffffu, mbar_wait(bar(L::B_Q_EMPTY + qs), ((qn >> 1) - 1) & 1, ctl))) break;
-        if (lane < NQ) {
-          uint8_t* dst = sptr + L::Q_OFF + qs * L::Q_BYTES + lane * L::ROW_BYTES;
-          const int sw = L::ROW_BYTES == 128 ? (lane & 7) : ((lane >> 1) & 3);
-          const float scale = __uint_as_float(up << 23);
+      if constexpr (KV8) {
+        if (it.n_loads > 0) {
+          for (; j < it.n_loads && vn < L::ST; ++j) load_v();  // (the first blocks, while the ring is empty)
+          const int qs = qn & 1;
+          if (qn >= 2 && !__all_sync(0xffffffffu, mbar_wait(bar(L::B_Q_EMPTY + qs), ((qn >> 1) - 1) & 1, ctl))) break;
+          ++qn;
+          // 16 dims of a row per lane, D / 16 lanes side by side on a row; a loop, not unrolled: this runs once or
+          // twice per CTA, and fetching its instructions is what it costs (unrolled over a whole row: 10k clk)
+          constexpr int LANES = D / 16;
+          uint8_t* const tile = sptr + L::Q_OFF + qs * L::Q_BYTES;
+          const int ch = lane % LANES;
+#pragma unroll 1
+          for (int r = lane / LANES; r < NQ; r += 32 / LANES) {
+            const bool real = r < p.group * it.n_pos;
+            uint32_t x[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+            if (real) {
+              const int pos = r / p.group;
+              const uint4* src = reinterpret_cast<const uint4*>(p.q + (static_cast<long long>(it.row0) + pos) * p.q_stride +
+                                                                static_cast<long long>(it.head * p.group + r - pos * p.group) * D) +
+                                 2 * ch;
+              const uint4 w0 = src[0], w1 = src[1];
+              x[0] = w0.x, x[1] = w0.y, x[2] = w0.z, x[3] = w0.w, x[4] = w1.x, x[5] = w1.y, x[6] = w1.z, x[7] = w1.w;
+            }
+            // the power of two that puts the row's largest element into [128, 256)
+            uint32_t most = 0;
 #pragma unroll
-          for (int ch = 0; ch < (KV8 ? D / 16 : 0); ++ch) {
+            for (int i = 0; i < 8; ++i) most = max(most, max(x[i] & 0x7f80u, (x[i] >> 16) & 0x7f80u));
+#pragma unroll
+            for (int off = LANES / 2; off > 0; off >>= 1) most = max(most, __shfl_xor_sync(0xffffffffu, most, off));
+            const uint32_t up = q_power(most);
+            const float scale = __uint_as_float(up << 23);
             uint32_t hi[4], lo[4];
-            const uint32_t x[8] = {w[2 * ch].x,     w[2 * ch].y,     w[2 * ch].z,     w[2 * ch].w,
-                                   w[2 * ch + 1].x, w[2 * ch + 1].y, w[2 * ch + 1].z, w[2 * ch + 1].w};
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               uint32_t h0, l0, h1, l1;
@@ -430,15 +441,17 @@ __global__ void __launch_bounds__(FewLayout<D, KV8, NQ>::THREADS, 1)
               hi[i] = h0 | (h1 << 16);
               lo[i] = l0 | (l1 << 16);
             }
-            *reinterpret_cast<uint4*>(dst + ((ch ^ sw) * 16)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-            // (lo terms: 16 times the remainder)
-            *reinterpret_cast<uint4*>(dst + L::Q_COL + ((ch ^ sw) * 16)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+            const int sw = L::ROW_BYTES == 128 ? (r & 7) : ((r >> 1) & 3);
+            uint8_t* dst = tile + r * L::ROW_BYTES + ((ch ^ sw) * 16);
+            *reinterpret_cast<uint4*>(dst) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+            *reinterpret_cast<uint4*>(dst + L::Q_COL) = make_uint4(lo[0], lo[1], lo[2], lo[3]);  // (16 times the remainder)
+            if (ch == 0)
+              reinterpret_cast<float*>(sptr + L::CQ_OFF)[(u % L::NI) * NQ + r] = real ? q_factor(p.scale_log2, up) : 0.f;
           }
+          fence_proxy_async_smem();
+          __syncwarp();
         }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(L::B_Q_FULL + qs));
-        ++qn;
+        if (lane == 0) mbar_arrive(bar(L::B_Q_FULL + u % L::NI));
       }
       for (; ok && j < it.n_loads; ++j) load_v();
     }
@@ -479,6 +492,7 @@ __global__ void __launch_bounds__(FewLayout<D, KV8, NQ>::THREADS, 1)
         m[q] = q < real ? kNoKeyYet : -kNoKeyYet;
         l[q] = 0.f;
       }
+      if (KV8 && nb > 0) wait_for(L::B_Q_FULL + u % L::NI, u / L::NI);  // (the factors of the scores)
       bool first = true;  // no block of this stream yet
       for (int gg = g; gg < g + nb; ++gg) {
         if ((gg & 1) != t) continue;

@@ -6,8 +6,8 @@
 // where it sees none: its rows still get their zeros), two steps a block where both
 // tiles work on it and one where the tokens fit one tile (a block of the chunk kernel takes 2.9 us for two
 // tiles, 1.2 us for one).  All units' steps form one
-// line, ordered by sequence, kv head, unit, each with an even number; CTA c takes the c-th of gridDim.x
-// equal stretches (of even length: no block is cut), so the loads are even whatever the lengths: a ragged batch, one long
+// line, ordered by sequence, kv head, unit; CTA c takes the c-th of gridDim.x
+// equal stretches (units and stretches of an even length where a block may be two steps: no block is cut), so the loads are even whatever the lengths: a ragged batch, one long
 // sequence, chunks beside single tokens.  A unit cut by a stretch's end is
 // computed in pieces, each left in the workspace as fp32 rows normalized over
 // the piece's keys with their log-sum-exp, and joined by paged_merge_kernel.
@@ -28,7 +28,8 @@ struct PagedParams {
   float* lse;
   int n_tokens, H_q, H_kv, group;
   long long q_stride;
-  int n_pages, page_size, max_pages, n_seq;
+  int n_pages, page_size, n_seq;
+  int room;                    // keys that a row of the page table has pages for
   int box_rows, box_shift;     // keys of one TMA box: the largest power of two that divides page_size, at most 128
   long long table_stride;
   const int *page_table, *seq_len, *q_start;
@@ -37,8 +38,9 @@ struct PagedParams {
   int causal;
   int tile_pos, unit_pos;      // tokens of a tile, of a unit
   int unit_rows;               // rows of a unit's partial result
-  int unit_extra;              // steps that stand for a unit's start and end (even)
-  int min_steps;               // least steps of a CTA's stretch
+  int step_log2;               // a block of a unit of two tiles is 2^step_log2 steps (units of one tile only: 0)
+  int unit_extra;              // steps that stand for a unit's start and end (a multiple of 2^step_log2)
+  int min_steps;               // least steps of a CTA's stretch (likewise)
   float* o_part;               // [2 gridDim.x, unit_rows, D]
   float* l_part;               // [2 gridDim.x, unit_rows], base-2 log-sum-exp
   int4* cut;                   // [2 gridDim.x]: the unit that stretch c starts inside of (CutUnit)
@@ -69,13 +71,12 @@ struct SeqWork {
 __device__ __forceinline__ SeqWork seq_work(const PagedParams& p, int b) {
   SeqWork w;
   const int qs = p.q_start[b], qe = p.q_start[b + 1], len = p.seq_len[b];
-  const long long room = static_cast<long long>(p.max_pages) * p.page_size;
   w.qs = max(0, min(qs, p.n_tokens));
   w.n_new = max(0, min(qe, p.n_tokens) - w.qs);
-  w.len = static_cast<int>(max(0ll, min(static_cast<long long>(len), room)));
+  w.len = max(0, min(len, p.room));
   w.bad = w.qs != qs || qe < qs || qe > p.n_tokens || w.len != len;
   w.diag = w.len - w.n_new;
-  w.units = (w.n_new + p.unit_pos - 1) / p.unit_pos;
+  w.units = w.n_new > p.unit_pos ? (w.n_new + p.unit_pos - 1) / p.unit_pos : (w.n_new > 0 ? 1 : 0);
   return w;
 }
 
@@ -88,9 +89,16 @@ __device__ __forceinline__ int blocks_to(const PagedParams& p, const SeqWork& w,
 __device__ __forceinline__ bool one_tile(const PagedParams& p, const SeqWork& w, int u) {
   return w.n_new - u * p.unit_pos <= p.tile_pos;
 }
-__device__ __forceinline__ int unit_steps(const PagedParams& p, const SeqWork& w, int u) {
+// How a unit's blocks become steps: a number added for its start and end, and the multiple it is rounded up to.
+struct UnitSteps {
+  int extra, round;
+};
+__device__ __forceinline__ int unit_steps(const PagedParams& p, const SeqWork& w, int u, UnitSteps as) {
   const int blocks = max(1, blocks_to(p, w, (u + 1) * p.unit_pos));
-  return (one_tile(p, w, u) ? (blocks + 1) & ~1 : 2 * blocks) + p.unit_extra;
+  int steps = blocks << p.step_log2;
+  if (one_tile(p, w, u)) steps = (blocks + p.step_log2) & ~p.step_log2;  // (even where a block may be two steps)
+  steps += as.extra;
+  return as.round > 1 ? (steps + as.round - 1) / as.round * as.round : steps;
 }
 
 __device__ __forceinline__ long long warp_sum(long long x) {
@@ -101,11 +109,12 @@ __device__ __forceinline__ long long warp_sum(long long x) {
 
 // Steps of one kv head of each lane's sequence (0 past the last): a lane counts few
 // units by itself; the warp counts a long chunk's together.
-__device__ __forceinline__ long long head_steps(const PagedParams& p, const SeqWork& w, int lane) {
+__device__ __forceinline__ long long head_steps(const PagedParams& p, const SeqWork& w, int lane, UnitSteps as) {
   long long mine = 0;
   const bool many = w.units > 8;
   if (!many)
-    for (int u = 0; u < w.units; ++u) mine += unit_steps(p, w, u);
+#pragma unroll 1
+    for (int u = 0; u < w.units; ++u) mine += unit_steps(p, w, u, as);
   for (unsigned left = __ballot_sync(0xffffffffu, many); left; left &= left - 1) {
     const int src = __ffs(left) - 1;
     SeqWork o;
@@ -114,7 +123,7 @@ __device__ __forceinline__ long long head_steps(const PagedParams& p, const SeqW
     o.diag = __shfl_sync(0xffffffffu, w.diag, src);
     o.units = __shfl_sync(0xffffffffu, w.units, src);
     long long part = 0;
-    for (int u = lane; u < o.units; u += 32) part += unit_steps(p, o, u);
+    for (int u = lane; u < o.units; u += 32) part += unit_steps(p, o, u, as);
     part = warp_sum(part);
     if (lane == src) mine = part;
   }
@@ -125,6 +134,7 @@ __device__ __forceinline__ long long head_steps(const PagedParams& p, const SeqW
 struct PagedWalk {
   long long at, end;  // next step, end of the stretch
   long long per;      // steps of a stretch
+  UnitSteps as;
   int b, head, u, step;  // where `at` is: sequence, kv head, unit, step of the unit
   SeqWork w;          // sequence b's
 };
@@ -136,35 +146,63 @@ __device__ __forceinline__ long long quotient(long long x, long long d) {
 }
 
 __device__ __forceinline__ void paged_walk_start(const PagedParams& p, PagedWalk& k, int cta, int n_ctas, int lane) {
-  long long total = 0;
-  SeqWork w{};             // the lane's sequence of the 32 read last, its steps per head, and
-  long long per_head = 0;  // the steps of the lanes up to it (inclusive)
-  long long upto = 0;
+  long long total = 0, units = 0;
+  SeqWork w{};  // the lane's sequence of the 32 read last
   auto read = [&](int b0) {
     w = SeqWork{};
     if (b0 + lane < p.n_seq) w = seq_work(p, b0 + lane);
-    per_head = head_steps(p, w, lane);
+  };
+  k.as = UnitSteps{0, 1};
+  for (int b0 = 0; b0 < p.n_seq; b0 += 32) {
+    read(b0);
+    if (w.bad && cta == 0) atomicExch(p.status, kDevBadIndex);
+    total += warp_sum(head_steps(p, w, lane, k.as)) * p.H_kv;
+    units += warp_sum(w.units) * p.H_kv;
+  }
+  k.per = max(quotient(total + n_ctas - 1, n_ctas), static_cast<long long>(p.min_steps));
+  k.per = (k.per + p.step_log2) & ~static_cast<long long>(p.step_log2);
+  // A second piece costs a CTA about as much as kPieceBlocks blocks.  Few units: if stretches that much longer at
+  // most can hold one piece each -- units rounded up to whole stretches -- they do (one sequence of 8000 keys, 8 kv
+  // heads: 14.1 us, else 18.1).  Many: a unit's start and end count as steps of their own (64 sequences of up to 1000
+  // keys: 49 us without, 38 with four).
+  constexpr int kPieceBlocks = 3;
+  bool whole = false;
+  if (p.n_seq <= 32 && units <= n_ctas && k.per <= 16 << p.step_log2) {
+    for (int i = 0; i <= kPieceBlocks && !whole; ++i) {
+      const long long per = k.per + (static_cast<long long>(i) << p.step_log2);
+      if (per > (1 << 28)) break;
+      const UnitSteps as{0, static_cast<int>(per)};
+      const long long t = warp_sum(head_steps(p, w, lane, as)) * p.H_kv;
+      if (t <= per * n_ctas) {
+        whole = true;
+        k.as = as;
+        k.per = per;
+        total = t;
+      }
+    }
+  }
+  if (!whole && total >= static_cast<long long>(n_ctas) * p.unit_extra) {
+    k.as.extra = p.unit_extra;
+    total += units * p.unit_extra;
+    k.per = quotient(total + n_ctas - 1, n_ctas);
+    k.per = (k.per + p.step_log2) & ~static_cast<long long>(p.step_log2);
+  }
+  k.at = min(k.per * cta, total);
+  k.end = min(k.at + k.per, total);
+  k.b = k.head = k.u = k.step = 0;
+  if (k.at >= k.end) return;
+  long long before = 0;      // steps of the sequences before b0
+  long long per_head, upto;  // a head's steps of the lane's sequence, and those of the lanes up to it (inclusive)
+  int b0 = 0;
+  while (true) {
+    if (p.n_seq > 32) read(b0);  // (32 sequences or fewer are still held)
+    per_head = head_steps(p, w, lane, k.as);
     upto = per_head * p.H_kv;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
       const long long x = __shfl_up_sync(0xffffffffu, upto, off);
       if (lane >= off) upto += x;
     }
-  };
-  for (int b0 = 0; b0 < p.n_seq; b0 += 32) {
-    read(b0);
-    if (w.bad && cta == 0) atomicExch(p.status, kDevBadIndex);
-    total += __shfl_sync(0xffffffffu, upto, 31);
-  }
-  k.per = (max(quotient(total + n_ctas - 1, n_ctas), static_cast<long long>(p.min_steps)) + 1) & ~1ll;
-  k.at = min(k.per * cta, total);
-  k.end = min(k.at + k.per, total);
-  k.b = k.head = k.u = k.step = 0;
-  if (k.at >= k.end) return;
-  long long before = 0;  // steps of the sequences before b0
-  int b0 = 0;
-  while (true) {
-    if (p.n_seq > 32) read(b0);  // (32 sequences or fewer are still held)
     if (__any_sync(0xffffffffu, before + upto > k.at) || b0 + 32 >= p.n_seq) break;
     before += __shfl_sync(0xffffffffu, upto, 31);
     b0 += 32;
@@ -183,7 +221,7 @@ __device__ __forceinline__ void paged_walk_start(const PagedParams& p, PagedWalk
   k.w.units = __shfl_sync(0xffffffffu, w.units, src);
   // the unit that holds step r of the head: 32 units at a time
   for (int u0 = 0;; u0 += 32) {
-    const int steps = u0 + lane < k.w.units ? unit_steps(p, k.w, u0 + lane) : 0;
+    const int steps = u0 + lane < k.w.units ? unit_steps(p, k.w, u0 + lane, k.as) : 0;
     int sum = steps;
     if (k.w.units > 1) {
 #pragma unroll
@@ -210,10 +248,10 @@ __device__ __forceinline__ PagedItem paged_walk_next(const PagedParams& p, Paged
   it.row0 = -1;
   it.slot = -1;
   if (k.at >= k.end) return it;
-  const int steps = unit_steps(p, k.w, k.u);
+  const int steps = unit_steps(p, k.w, k.u, k.as);
   const int take = static_cast<int>(min(static_cast<long long>(steps - k.step), k.end - k.at));
   it.dual = one_tile(p, k.w, k.u);
-  const int scale = it.dual ? 0 : 1;  // log2 of the steps of a block
+  const int scale = it.dual ? 0 : p.step_log2;  // log2 of the steps of a block
   const int q0 = k.u * p.unit_pos;
   it.row0 = k.w.qs + q0;
   it.n_pos = min(p.unit_pos, k.w.n_new - q0);
@@ -264,7 +302,7 @@ __device__ __forceinline__ int4 paged_cut(const PagedParams& p, const PagedWalk&
   const long long start = k.at - k.step;
   if (start < (cta - 1) * k.per) return make_int4(-1, 0, 0, 0);
   const int q0 = k.u * p.unit_pos;
-  const long long last = quotient(start + unit_steps(p, k.w, k.u) - 1, k.per);
+  const long long last = quotient(start + unit_steps(p, k.w, k.u, k.as) - 1, k.per);
   return make_int4(k.w.qs + q0, min(p.unit_pos, k.w.n_new - q0), k.head, static_cast<int>(last));
 }
 
@@ -272,11 +310,11 @@ __device__ __forceinline__ int4 paged_cut(const PagedParams& p, const PagedWalk&
 // that stretch c + 1 starts inside of: pieces 2 c + 1 and 2 c', c' = c + 1 .. last.
 //   lse = log2 sum_s 2^(lse_s),   O = sum_s 2^(lse_s - lse) O_s
 // It is a chain of reads (the record, then the pieces), so their latency counts: a warp asks for the pieces of
-// its ROWS rows, four at a time each, together (four rows a warp for the chunk kernel's 256-row units: one row
-// a warp took 30 us for 147 cut units, in eight waves of blocks).  More than eight pieces (a long sequence over
+// its rows, W at a time each, together (four rows a warp for the chunk kernel's 256-row units: one row
+// a warp took 30 us for 147 cut units, in eight waves of blocks).  More than 2 W pieces (a long sequence over
 // many CTAs) are shared out among the block's eight warps, row by row.  The order of the sums depends on the
 // lengths only.
-template <int D, int ROWS>
+template <int D, int ROWS, int W>
 struct MergeRows {
   static constexpr int PER = D / 32;
   using Vec = typename std::conditional<PER == 4, float4, float2>::type;
@@ -292,15 +330,15 @@ struct MergeRows {
     }
   }
 
-  // adds pieces first, first + step, ... below n (at most four of them) of rows r, r + 1, ...
+  // adds pieces first, first + step, ... below n (at most W of them) of rows r, r + 1, ...
   template <typename Place>
   __device__ __forceinline__ void add(const PagedParams& p, int r, int lane, int first, int step, int n, Place place) {
-    float l[ROWS][4];
-    Vec v[ROWS][4];
+    float l[ROWS][W];
+    Vec v[ROWS][W];
 #pragma unroll
     for (int i = 0; i < ROWS; ++i) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
+      for (int j = 0; j < W; ++j) {
         const int s = first + j * step;
         l[i][j] = -INFINITY;
         if (s < n) {
@@ -312,14 +350,16 @@ struct MergeRows {
     }
 #pragma unroll
     for (int i = 0; i < ROWS; ++i) {
-      const float top = fmaxf(fmaxf(fmaxf(l[i][0], l[i][1]), fmaxf(l[i][2], l[i][3])), m[i]);
+      float top = m[i];
+#pragma unroll
+      for (int j = 0; j < W; ++j) top = fmaxf(top, l[i][j]);
       if (top == -INFINITY) continue;  // no piece so far saw a key
       const float old = m[i] == -INFINITY ? 0.f : exp2_mufu(m[i] - top);
       sum[i] *= old;
 #pragma unroll
       for (int x = 0; x < PER; ++x) acc[i][x] *= old;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
+      for (int j = 0; j < W; ++j) {
         if (l[i][j] == -INFINITY) continue;
         const float w = exp2_mufu(l[i][j] - top);
         sum[i] += w;
@@ -346,7 +386,7 @@ __host__ __device__ constexpr int merge_rows(int tile_rows) { return tile_rows =
 
 template <int D, int TILE_ROWS>
 __global__ void __launch_bounds__(256) paged_merge_kernel(const PagedParams p) {
-  constexpr int PER = D / 32, ROWS = merge_rows(TILE_ROWS);
+  constexpr int PER = D / 32, ROWS = merge_rows(TILE_ROWS), W = ROWS == 1 ? 8 : 4;
   __shared__ __align__(16) float red_o[8][D];
   __shared__ float red_m[8], red_l[8];
   // a programmatic dependent of the attention kernel: waits for its results
@@ -372,22 +412,22 @@ __global__ void __launch_bounds__(256) paged_merge_kernel(const PagedParams p) {
   };
   const int r0 = blockIdx.y * 8 * ROWS;
   int pos, head;
-  if (n <= 8) {
+  if (n <= 2 * W) {
     const int r = r0 + warp * ROWS;
     bool any = false;  // (padding rows hold no partial result: they are read, and dropped)
 #pragma unroll
     for (int i = 0; i < ROWS; ++i) any |= unit_row<TILE_ROWS>(p, r + i, cut.y, pos, head);
     if (!any) return;
-    MergeRows<D, ROWS> rows;
+    MergeRows<D, ROWS, W> rows;
     rows.add(p, r, lane, 0, 1, n, place);
-    if (n > 4) rows.add(p, r, lane, 4, 1, n, place);
+    if (n > W) rows.add(p, r, lane, W, 1, n, place);
 #pragma unroll
     for (int i = 0; i < ROWS; ++i) finish(r + i, rows.m[i], rows.sum[i], rows.acc[i]);
     return;
   }
   for (int r = r0; r < r0 + 8 * ROWS; ++r) {
     if (!unit_row<TILE_ROWS>(p, r, cut.y, pos, head)) continue;  // (the same for the whole block)
-    MergeRows<D, 1> row;
+    MergeRows<D, 1, 4> row;
     for (int s = warp; s < n; s += 32) row.add(p, r, lane, s, 8, n, place);
 #pragma unroll
     for (int x = 0; x < PER; ++x) red_o[warp][lane * PER + x] = row.acc[0][x];
