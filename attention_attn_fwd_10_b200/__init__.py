@@ -314,6 +314,8 @@ class FwdBwdPipeline:
         self.scale = 1.0 / math.sqrt(D) if scale is None else float(scale)
         self.up, self.compute, self.down = (torch.cuda.Stream(self.dev) for _ in range(3))
         bf, dev = torch.bfloat16, self.dev
+        if rotary is not None:  # refuse here what the first submit would
+            rotary._struct(positions, B * S_q, torch.empty(0, device=dev).device)
         ws = bwd_workspace_size(B, H_q, S_q, D)
         self.sets = []
         for _ in range(max(1, int(depth))):

@@ -45,25 +45,6 @@ attn_status_t set_rotary(RotaryParams* p, const attn_rotary_t* r, int D, bool in
   return ATTN_OK;
 }
 
-// Launches a kernel as a programmatic dependent of the one before it on the stream: its blocks may start as that
-// one's last blocks finish, and wait on the device (griddepcontrol.wait) before they touch memory.  A layer's
-// append, attention and merge are short kernels in a row, whose launch and set-up overlap so.
-template <typename... Params, typename... Args>
-cudaError_t launch_dependent(void (*kern)(Params...), dim3 grid, unsigned threads, size_t smem, cudaStream_t s,
-                             const Args&... args) {
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, args...);
-}
-
 template <int D, int VEC, bool INTERLEAVED, bool PAGED, bool E4M3>
 cudaError_t launch_rotary(RotaryParams p, cudaStream_t s) {
   constexpr int ITEMS = 4;
@@ -81,8 +62,9 @@ cudaError_t launch_rotary(RotaryParams p, cudaStream_t s) {
   const long long gx = (p.n_tokens + tok - 1) / tok;
   const int gy = (p.n_heads + hpc - 1) / hpc;
   if (gx > 2147483647ll || gy > 65535) return cudaErrorInvalidConfiguration;
-  return launch_dependent(rotary_kernel<D, VEC, ITEMS, INTERLEAVED, PAGED, E4M3>,
-                          dim3(static_cast<unsigned>(gx), static_cast<unsigned>(gy)), kRotThreads, 0, s, p);
+  rotary_kernel<D, VEC, ITEMS, INTERLEAVED, PAGED, E4M3>
+      <<<dim3(static_cast<unsigned>(gx), static_cast<unsigned>(gy)), kRotThreads, 0, s>>>(p);
+  return cudaGetLastError();
 }
 
 // 16-byte chunks need frequencies in eights; else (rotated dims such as 24) 8-byte ones.
@@ -221,10 +203,21 @@ cudaError_t launch_paged(void (*kern)(CUtensorMap, CUtensorMap, CUtensorMap, Pag
   if (!make_cache_map(&mk, c, c->k, p.box_rows) || !make_cache_map(&mv, c, c->v, p.box_rows)) return cudaErrorUnknown;
   cudaError_t e = api_smem_opt_in(reinterpret_cast<const void*>(kern), L::SMEM_BYTES, seen);
   if (e != cudaSuccess) return e;
-  e = launch_dependent(kern, dim3(kPagedCtas), L::THREADS, L::SMEM_BYTES, s, mq, mk, mv, p);
+  kern<<<kPagedCtas, L::THREADS, L::SMEM_BYTES, s>>>(mq, mk, mv, p);
+  e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  return launch_dependent(paged_merge_kernel<D, TILE_ROWS>, dim3(kPagedCtas - 1, static_cast<unsigned>(p.unit_rows / (8 * merge_rows(TILE_ROWS)))),
-                          256, 0, s, p);
+  // the merge: a programmatic dependent, so that its launch overlaps the attention's tail (it waits on the device for
+  // that grid, and so for everything before it)
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(kPagedCtas - 1, static_cast<unsigned>(p.unit_rows / (8 * merge_rows(TILE_ROWS))));
+  cfg.blockDim = dim3(256);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, paged_merge_kernel<D, TILE_ROWS>, p);
 }
 
 // The kernel by the rows that a sequence's new tokens make in a kv group (max_new, or the mean where it is not
@@ -356,7 +349,7 @@ attn_status_t attn_fwd_paged(const attn_paged_kv_t* c, const void* q, void* o, f
     return ATTN_ERR_INVALID_ARG;
   if (max_new < 0 || (causal != 0 && causal != 1) || !std::isfinite(scale) || !(scale > 0.f)) return ATTN_ERR_INVALID_ARG;
   if (H_q / c->H_kv > 128) return ATTN_ERR_UNSUPPORTED;
-  if (!aligned(q, 16) || !aligned(o, 16) || !aligned(lse, 16) || !aligned(workspace, 16)) return ATTN_ERR_MISALIGNED;
+  if (!aligned(q, 16) || !aligned(o, 16) || !aligned(lse, 16) || !aligned(workspace, 32)) return ATTN_ERR_MISALIGNED;
   if (n_tokens == 0) return ATTN_OK;
   PagedParams p{};
   p.status = api_status_ptr();

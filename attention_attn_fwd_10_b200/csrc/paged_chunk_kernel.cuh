@@ -176,7 +176,7 @@ __global__ void __launch_bounds__(ChunkLayout<D, KV8>::THREADS, 1)
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
   const int cta = static_cast<int>(blockIdx.x);
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the merge kernel, which waits for this grid
 
   // ---- setup
   if (threadIdx.x == 0) {
@@ -203,9 +203,7 @@ __global__ void __launch_bounds__(ChunkLayout<D, KV8>::THREADS, 1)
   }
   PagedWalk walk;
   if (warp == L::WARP_SCHED) {
-    // the CTA's stretch, while the others set up; a programmatic dependent of the kernel before it: nothing that
-    // kernel may have written is read before this wait, and the other roles start on what this warp publishes
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    // the CTA's stretch, while the others set up
     paged_walk_start(p, walk, cta, static_cast<int>(gridDim.x), lane);
   }
   tc_fence_before();

@@ -180,7 +180,7 @@ __global__ void __launch_bounds__(FewLayout<D, KV8, NQ>::THREADS, 1)
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
   const int cta = static_cast<int>(blockIdx.x);
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the merge kernel, which waits for this grid
 
   // ---- setup
   if (threadIdx.x == 0) {
@@ -208,8 +208,7 @@ __global__ void __launch_bounds__(FewLayout<D, KV8, NQ>::THREADS, 1)
   if (threadIdx.x < NQ) reinterpret_cast<int*>(sptr + L::POS_OFF)[threadIdx.x] = static_cast<int>(threadIdx.x) / p.group;
   PagedWalk walk;
   if (warp == L::WARP_SCHED) {
-    // the CTA's stretch, while the others set up (as in the chunk kernel)
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    // the CTA's stretch, while the others set up
     paged_walk_start(p, walk, cta, static_cast<int>(gridDim.x), lane);
   }
   fence_proxy_async_smem();

@@ -390,7 +390,6 @@ __global__ void __launch_bounds__(256) paged_merge_kernel(const PagedParams p) {
   __shared__ __align__(16) float red_o[8][D];
   __shared__ float red_m[8], red_l[8];
   // a programmatic dependent of the attention kernel: waits for its results
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int c = blockIdx.x + 1;
   const int4 cut = p.cut[c];

@@ -127,9 +127,6 @@ __global__ void __launch_bounds__(kRotThreads) rotary_kernel(const RotaryParams 
   const int nh = min(p.hpc, p.n_heads - h0);
   const int n_items = nt * nh * PER_HEAD;
   const int fv = p.n_freq / VEC;  // rotated items of a head
-  // a programmatic dependent of the kernel before it, as the next one may be of this
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  asm volatile("griddepcontrol.wait;" ::: "memory");
 
   // where item `it` is: token, head list entry, chunks
   struct Item {

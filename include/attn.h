@@ -299,15 +299,17 @@ attn_status_t attn_paged_append(const attn_paged_kv_t* cache, const void* q, con
  * (bf16, contiguous) and lse [H_q, n_tokens] (fp32, natural log).  Causal: new token i of n of a
  * sequence of L keys sees keys 0 .. L - n + i; else all L.  Rows that see no key get
  * O = 0, lse = -inf.  One token per sequence (decoding) and chunks of a prompt may
- * be mixed in one call.  Cache slots from a sequence's end on are never used,
- * whatever they hold; the keys and values before it must be finite.  The e4m3 cache's
- * products run on the 8-bit tensor-core path with q and the softmax weights as sums of
- * two e4m3 terms, so they are as exact as with bf16.
+ * be mixed in one call.  Cache slots from a sequence's end on are never used, whatever
+ * they hold; q and the keys and values before it must be finite.  An e4m3 cache costs
+ * no accuracy beyond its own rounding: its K and V are used as they are, q and the softmax
+ * weights with 8 bits or more, as with bf16 (as sums of two e4m3 terms on the 8-bit
+ * tensor-core path, or as fp16); where the rows of a kv group are few, a weight may be off by 2^-17 of the
+ * row's largest besides.  The same call on the same lengths gives the same bits.
  *   q        : bf16, token stride q_stride elements (a multiple of 8, >= H_q * D).
  *   H_q      : a multiple of the cache's H_kv, H_q / H_kv <= 128.
  *   max_new  : the most new tokens of any sequence, as far as the caller knows: it
  *              chooses the kernel, and any value gives the same result up to rounding.  0 = unknown.
- *   workspace: device, 16-byte aligned, attn_fwd_paged_workspace_size(H_q, H_kv, D)
+ *   workspace: device, 32-byte aligned, attn_fwd_paged_workspace_size(H_q, H_kv, D)
  *              bytes; contents ignored, none kept.  Calls that may overlap need one each.
  */
 attn_status_t attn_fwd_paged(const attn_paged_kv_t* cache, const void* q, void* o, float* lse, void* workspace,

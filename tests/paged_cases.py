@@ -55,7 +55,7 @@ def handle(attn, g):
                         k_scale=g["k_scale"], v_scale=g["v_scale"])
 
 
-def check_attend(o, lse, want, rows, what="", e4m3=True, score_error=0.0):
+def check_attend(o, lse, want, rows, what="", e4m3=False, score_error=0.0):
     """o and lse against the oracle's (o, lse, a) on the given token rows.
 
     o: the output's rounding (half a bf16 step: 2^-8 relative), each softmax weight's rounding to bf16, or

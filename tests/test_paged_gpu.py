@@ -145,7 +145,7 @@ def test_attend_lengths(e4m3, D, new, keys):
     x = make(new, keys, 8, 2, D, 16, e4m3=e4m3, seed=sum(keys) + D)
     for causal in (True, False):
         o, lse, want = _attend(x, causal, max_new=max(new))
-        check_attend(o, lse, want, _rows(x), f"causal={causal}")
+        check_attend(o, lse, want, _rows(x), f"causal={causal}", e4m3=e4m3)
 
 
 @pytest.mark.parametrize("e4m3", [False, True])
@@ -155,7 +155,7 @@ def test_attend_lengths(e4m3, D, new, keys):
 def test_attend_heads(e4m3, H_q, H_kv, new, keys):
     x = make(new, keys, H_q, H_kv, 128, 32, e4m3=e4m3, seed=H_q)
     o, lse, want = _attend(x, max_new=max(new))
-    check_attend(o, lse, want, _rows(x))
+    check_attend(o, lse, want, _rows(x), e4m3=bool(x["k_scale"] != 1.0))
 
 
 @pytest.mark.parametrize("e4m3", [False, True])
@@ -163,7 +163,7 @@ def test_attend_heads(e4m3, H_q, H_kv, new, keys):
 def test_attend_pages(e4m3, page):
     x = make([1, 150, 2], [500, 300, 1030], 4, 2, 128, page, e4m3=e4m3, seed=page)
     o, lse, want = _attend(x)
-    check_attend(o, lse, want, _rows(x))
+    check_attend(o, lse, want, _rows(x), e4m3=bool(x["k_scale"] != 1.0))
 
 
 @pytest.mark.parametrize("hint", [0, 1, 3, 8, 1000000])
@@ -171,7 +171,7 @@ def test_attend_any_hint(hint):
     # the hint chooses the kernel; more new tokens than it says are served all the same
     x = make([3, 1, 70, 300], [900, 128, 70, 513], 8, 2, 128, 64, seed=hint % 97)
     o, lse, want = _attend(x, max_new=hint)
-    check_attend(o, lse, want, _rows(x))
+    check_attend(o, lse, want, _rows(x), e4m3=bool(x["k_scale"] != 1.0))
 
 
 @pytest.mark.parametrize("hint", [1, 400])
@@ -180,7 +180,7 @@ def test_attend_rows_without_keys(hint, e4m3):
     # no keys at all; more new tokens than keys (the first see none)
     x = make([2, 300, 1, 40], [0, 100, 1, 7], 4, 1, 128, 16, e4m3=e4m3, seed=4)
     o, lse, want = _attend(x, max_new=hint)
-    check_attend(o, lse, want, _rows(x))
+    check_attend(o, lse, want, _rows(x), e4m3=bool(x["k_scale"] != 1.0))
     assert torch.all(o[:2] == 0) and torch.all(torch.isneginf(lse[:, :2]))
     assert torch.all(o[2:202] == 0) and torch.all(torch.isneginf(lse[:, 2:202]))
 
@@ -194,7 +194,7 @@ def test_attend_leaves_other_rows(hint):
     out = torch.full(x["q"].shape, 7.0, dtype=torch.bfloat16, device="cuda")
     lse = torch.full((4, x["q"].shape[0]), 7.0, device="cuda")
     o, lse, want = _attend(x, out=out, lse=lse, max_new=hint)
-    check_attend(o, lse, want, _rows(x))
+    check_attend(o, lse, want, _rows(x), e4m3=bool(x["k_scale"] != 1.0))
     rest = np.setdiff1d(np.arange(x["q"].shape[0]), _rows(x))
     assert torch.all(o[rest] == 7) and torch.all(lse[:, rest] == 7)
 
@@ -207,7 +207,7 @@ def test_attend_many_sequences(e4m3):
     keys = [max(n, int(rng.integers(0, 400))) for n in new]
     x = make(new, keys, 4, 2, 64, 16, e4m3=e4m3, seed=6)
     o, lse, want = _attend(x)
-    check_attend(o, lse, want, _rows(x))
+    check_attend(o, lse, want, _rows(x), e4m3=bool(x["k_scale"] != 1.0))
 
 
 @pytest.mark.parametrize("e4m3", [False, True])
@@ -216,7 +216,7 @@ def test_attend_long(e4m3, new, keys):
     # one sequence split over every SM
     x = make(new, keys, 4, 1, 128, 64, e4m3=e4m3, seed=7)
     o, lse, want = _attend(x, max_new=max(new))
-    check_attend(o, lse, want, _rows(x))
+    check_attend(o, lse, want, _rows(x), e4m3=bool(x["k_scale"] != 1.0))
 
 
 @pytest.mark.parametrize("hint", [1, 400])
@@ -245,7 +245,7 @@ def test_attend_shared_pages_and_strided_layouts():
     # both sequences read the same pages (a common prefix, and here all of it)
     x["page_table"][1] = x["page_table"][0]
     o, lse, want = _attend(x)
-    check_attend(o, lse, want, _rows(x))
+    check_attend(o, lse, want, _rows(x), e4m3=bool(x["k_scale"] != 1.0))
     d = to_gpu(x)
     n = x["k_cache"].shape[0]
     pool = torch.empty((n, 2, 2, 16, 64), dtype=torch.bfloat16, device="cuda")
@@ -277,6 +277,120 @@ def test_attend_same_every_time_and_on_other_streams(hint, e4m3):
     for o, lse in [again, *more]:
         assert torch.equal(o, first[0]) and torch.equal(lse, first[1])
     assert attn.device_status() == 0
+
+
+@pytest.mark.parametrize("hint", [1, 400])
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_attend_many_ragged_chunks(hint, e4m3):
+    """Chunks and single tokens, more units than CTAs, lengths around the 128-key blocks."""
+    rng = np.random.default_rng(21)
+    new = [int(n) for n in rng.choice([1, 1, 2, 33, 64, 65, 127, 128, 129, 300], 40)]
+    keys = [n + int(k) for n, k in zip(new, rng.choice([0, 1, 63, 127, 128, 200, 500], 40))]
+    x = make(new, keys, 6, 2, 64, 48, e4m3=e4m3, seed=21)
+    for causal in (True, False):
+        o, lse, want = _attend(x, causal, max_new=hint)
+        check_attend(o, lse, want, _rows(x), f"causal={causal}", e4m3=e4m3)
+
+
+@pytest.mark.parametrize("hint", [1, 400])
+def test_attend_whole_and_shared_stretches(hint):
+    """Unit counts and lengths on both sides of the rules that lay the work out (short stretches of one piece,
+    long ones that hold several units)."""
+    for B, keys in ((1, 140), (1, 8000), (2, 2500), (7, 1111), (31, 515), (33, 515), (60, 1030)):
+        x = make([1] * B, [keys + 13 * b for b in range(B)], 4, 2, 128, 64, seed=B, poison=False)
+        o, lse, want = _attend(x, max_new=hint)
+        check_attend(o, lse, want, _rows(x), f"{B} x {keys}")
+
+
+def test_cache_beyond_32_bits():
+    """A pool of more than 2^32 bytes and 2^31 elements: pages at its far end."""
+    attn = _attn()
+    H_kv, D, page, n_pages = 8, 128, 128, 17000
+    assert n_pages * page * H_kv * D > 2 ** 31
+    x = make([3, 1], [300, 129], 16, H_kv, D, page, seed=22, poison=False)
+    g = to_gpu(x)
+    far = {}
+    for name in ("k_cache", "v_cache"):
+        far[name] = torch.empty((n_pages, page, H_kv, D), dtype=torch.bfloat16, device="cuda")
+        far[name][-g[name].shape[0]:] = g[name]
+    table = torch.where(g["page_table"] < 2 ** 29, g["page_table"] + n_pages - x["k_cache"].shape[0], g["page_table"])
+    cache = attn.PagedKV(far["k_cache"], far["v_cache"], table.contiguous(), g["seq_len"], g["q_start"])
+    o, lse = attn.fwd_paged(cache, g["q"])
+    want = attn.fwd_paged(handle(attn, g), g["q"])
+    assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
+    k = torch.randn((4, H_kv, D), generator=torch.Generator().manual_seed(1)).bfloat16().cuda()
+    v = -k
+    attn.paged_append(cache, k, v)
+    for t, _, _, pg, slot in oracle.slots(table.cpu().numpy(), x["keys"], x["start"], page):
+        assert pg > 16000
+        assert torch.equal(far["k_cache"][pg, slot], k[t]) and torch.equal(far["v_cache"][pg, slot], v[t])
+    assert attn.device_status() == 0
+
+
+def test_calls_from_several_threads():
+    import threading
+
+    attn = _attn()
+    xs = [make([1, 40], [700, 300 + 10 * i], 8, 2, 128, 16, e4m3=i % 2 == 1, seed=30 + i) for i in range(4)]
+    gs = [to_gpu(x) for x in xs]
+    want = [attn.fwd_paged(handle(attn, g), g["q"]) for g in gs]
+    torch.cuda.synchronize()
+    got = [[] for _ in xs]
+
+    def work(i):
+        s = torch.cuda.Stream()
+        cache = handle(attn, gs[i])
+        for _ in range(20):
+            got[i].append(attn.fwd_paged(cache, gs[i]["q"], stream=s))
+        s.synchronize()
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    for i in range(4):
+        assert len(got[i]) == 20
+        for o, lse in got[i]:
+            assert torch.equal(o, want[i][0]) and torch.equal(lse, want[i][1])
+    assert attn.device_status() == 0
+
+
+@pytest.mark.skipif(not torch.cuda.is_available() or torch.cuda.device_count() < 2, reason="needs two devices")
+def test_on_the_device_of_the_tensors():
+    attn = _attn()
+    x = make([1, 5], [300, 200], 4, 2, 128, 16, seed=40)
+    want = oracle.attend(x["q"], x["k_cache"], x["v_cache"], x["page_table"].numpy(), x["keys"], x["start"], True, 128 ** -0.5)
+    for d in (0, 1):
+        g = {n: t.to(f"cuda:{d}") if isinstance(t, torch.Tensor) else t for n, t in x.items()}
+        with torch.cuda.device(1 - d):  # the current device is another one
+            o, lse = attn.fwd_paged(handle(attn, g), g["q"])
+        torch.cuda.synchronize(d)
+        assert o.device.index == d
+        check_attend(o, lse, want, _rows(x), f"device {d}")
+
+
+@pytest.mark.parametrize("hint", [1, 20, 400])
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_waits_that_run_out_are_reported(hint, e4m3):
+    """With a limit of 1 ns per wait the kernels give up, report it and leave; the next call is right again."""
+    attn = _attn()
+    x = make([1, 200, 1], [3000, 900, 700], 8, 4, 128, 16, e4m3=e4m3, seed=41)
+    g = to_gpu(x)
+    cache = handle(attn, g)
+    want = attn.fwd_paged(cache, g["q"], max_new=hint)
+    assert attn.device_status() == 0
+    attn.set_wait_limit_ns(1)
+    try:
+        for _ in range(3):
+            attn.fwd_paged(cache, g["q"], max_new=hint)
+        status = attn.device_status()
+    finally:
+        attn.set_wait_limit_ns(0)
+    assert status == 5
+    o, lse = attn.fwd_paged(cache, g["q"], max_new=hint)
+    assert attn.device_status() == 0
+    assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
 
 
 @pytest.mark.parametrize("e4m3", [False, True])

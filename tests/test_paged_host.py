@@ -53,7 +53,7 @@ def test_other_layouts_pass_the_checks(lib):
 @pytest.mark.parametrize("kw,code", [
     (dict(q=0), 1), (dict(o=0), 1), (dict(lse=0), 1), (dict(ws=0), 1), (dict(T=-1), 1), (dict(H_q=3), 1), (dict(H_q=0), 1),
     (dict(stride=248), 1), (dict(stride=260), 1), (dict(max_new=-1), 1), (dict(causal=2), 1), (dict(scale=0.0), 1),
-    (dict(scale=float("inf")), 1), (dict(H_q=258, stride=258 * 64), 2), (dict(q=24), 3), (dict(ws=40), 3), (dict(lse=36), 3)])
+    (dict(scale=float("inf")), 1), (dict(H_q=258, stride=258 * 64), 2), (dict(q=24), 3), (dict(ws=40), 3), (dict(ws=48), 3), (dict(lse=36), 3)])
 def test_attend_refusals(lib, kw, code):
     a = dict(q=16, o=32, lse=48, ws=64, T=1, H_q=4, stride=256, max_new=0, causal=1, scale=0.125)
     a.update(kw)
