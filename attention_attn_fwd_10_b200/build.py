@@ -8,7 +8,8 @@ whose kernels record a per-block clock64 timeline of one chosen CTA
 (include/attn_timeline.h; read by attention_attn_fwd_10_b200.timeline).  It is a
 measurement aid, never loaded by the package unless asked for.
 
-nvcc cross-compiles without a GPU.  The library links the CUDA runtime
+nvcc cross-compiles without a GPU; each source is compiled by its own nvcc, side by
+side.  The library links the CUDA runtime
 statically and reaches the driver only through cudaGetDriverEntryPoint, so it
 needs no libcuda at link time.
 """
@@ -18,6 +19,7 @@ import os
 import shutil
 import subprocess
 import sys
+import tempfile
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -33,9 +35,10 @@ DEPS = SOURCES + [
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
     "-lineinfo", "-O3", "-std=c++17",
-    "-shared", "-Xcompiler", "-fPIC",
+    "-Xcompiler", "-fPIC",
     "-Xptxas", "-v",
 ]
+LINK_FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a", "-shared", "-Xcompiler", "-fPIC"]
 
 
 def nvcc_path() -> str:
@@ -56,13 +59,24 @@ def build(force: bool = False, verbose: bool = False, timeline: bool = False) ->
     lib = LIB_TIMELINE if timeline else LIB
     if not force and up_to_date(lib):
         return lib
-    cmd = [nvcc_path(), *NVCC_FLAGS, *(["-DATTN_TIMELINE"] if timeline else []), "-o", lib + ".tmp", *SOURCES]
-    res = subprocess.run(cmd, capture_output=True, text=True)
-    if res.returncode != 0:
-        raise RuntimeError("nvcc failed:\n" + res.stdout + res.stderr)
+    log = ""
+    with tempfile.TemporaryDirectory() as tmp:
+        objects = [os.path.join(tmp, os.path.basename(src) + ".o") for src in SOURCES]
+        defines = ["-DATTN_TIMELINE"] if timeline else []
+        # the sources side by side, then the link
+        jobs = [subprocess.Popen([nvcc_path(), *NVCC_FLAGS, *defines, "-c", "-o", obj, src], text=True,
+                                 stdout=subprocess.PIPE, stderr=subprocess.STDOUT) for src, obj in zip(SOURCES, objects)]
+        outs = [job.communicate()[0] for job in jobs]
+        for job, out in zip(jobs, outs):
+            log += out
+            if job.returncode != 0:
+                raise RuntimeError("nvcc failed:\n" + out)
+        res = subprocess.run([nvcc_path(), *LINK_FLAGS, "-o", lib + ".tmp", *objects], capture_output=True, text=True)
+        if res.returncode != 0:
+            raise RuntimeError("nvcc failed to link:\n" + res.stdout + res.stderr)
     os.replace(lib + ".tmp", lib)
     if verbose:
-        for line in (res.stdout + res.stderr).splitlines():
+        for line in log.splitlines():
             if "registers" in line or "spill" in line or "Compiling entry" in line:
                 print(line)
     return lib
