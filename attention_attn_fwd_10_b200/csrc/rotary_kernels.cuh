@@ -11,8 +11,11 @@
 // The work is bytes: each element is read and written once.  An item is two
 // chunks of VEC elements (16 bytes each for VEC = 8) that hold VEC whole pairs:
 // chunks (i, i + n_freq / VEC) of a head in the half layout, (2i, 2i + 1) in the
-// interleaved one.  A thread holds ITEMS items, all loads issued before the
-// angles are computed, so their latency overlaps.
+// interleaved one.  A thread holds ITEMS = 4 items, all loads issued before the
+// angles are computed, so their latency overlaps; four CTAs of 256 threads per SM.  It is
+// also near the issue rate (68 % with a division per item and access), so a thread's items share one.
+// q and k of 2 x 8192 tokens x 16 heads x 128, 269 MB: 44.2 us, 6.1 TB/s, 93 % of the measured copy rate
+// (3, 5, 6 CTAs per SM: 45.6, 50.2, 56.9 us; 2 items per thread: 50.6 us; 8: 56.7 us).
 #pragma once
 
 #include <cuda_fp8.h>
@@ -113,7 +116,7 @@ constexpr int kRotThreads = 256;
 constexpr int kRotMaxTok = 8;    // tokens of a CTA: one warp looks each one's sequence up
 
 template <int D, int VEC, int ITEMS, bool INTERLEAVED, bool PAGED, bool E4M3>
-__global__ void __launch_bounds__(kRotThreads) rotary_kernel(const RotaryParams p) {
+__global__ void __launch_bounds__(kRotThreads, 4) rotary_kernel(const RotaryParams p) {
   using V = typename RotVec<VEC>::T;
   constexpr int PER_HEAD = D / (2 * VEC);  // items of a head
   __shared__ __align__(16) float s_cos[kRotMaxTok * D / 2], s_sin[kRotMaxTok * D / 2];
@@ -125,51 +128,56 @@ __global__ void __launch_bounds__(kRotThreads) rotary_kernel(const RotaryParams 
   const int nt = static_cast<int>(min(static_cast<long long>(p.tok), p.n_tokens - t0));
   const int h0 = blockIdx.y * p.hpc;
   const int nh = min(p.hpc, p.n_heads - h0);
-  const int n_items = nt * nh * PER_HEAD;
   const int fv = p.n_freq / VEC;  // rotated items of a head
 
-  // where item `it` is: token, head list entry, chunks
-  struct Item {
-    int tau, which, head, i, ca, cb;
+  // Item u of a thread: the same chunks ca, cb of (token, head list entry) number pair0 + u STEP of the CTA, so that
+  // one division places all of them.
+  constexpr int STEP = kRotThreads / PER_HEAD;
+  static_assert(kRotThreads % PER_HEAD == 0, "a thread's items have the same chunks");
+  const int i = tid % PER_HEAD, pair0 = tid / PER_HEAD;
+  const int n_pairs = nt * nh;
+  int ca, cb;
+  if (INTERLEAVED || i >= fv) {
+    ca = 2 * i;  // (past the rotated ones, half layout: 2 fv + 2 (i - fv))
+    cb = ca + 1;
+  } else {
+    ca = i;
+    cb = i + fv;
+  }
+  struct Place {
+    int tau, h;            // token of the CTA, entry of its head range
+    int which, head;       // q, k or v, and the head there
   };
-  auto locate = [&](int it) {
-    Item w;
-    w.i = it % PER_HEAD;
-    const int th = it / PER_HEAD;
-    w.tau = th / nh;
-    int h = h0 + th - w.tau * nh;
+  auto settle = [&](Place& w) {
+    while (w.h >= nh) {
+      w.h -= nh;
+      ++w.tau;
+    }
     w.which = 0;
-    if (h >= p.heads[0]) {
-      h -= p.heads[0];
+    w.head = h0 + w.h;
+    if (w.head >= p.heads[0]) {
+      w.head -= p.heads[0];
       w.which = 1;
-      if (h >= p.heads[1]) {
-        h -= p.heads[1];
+      if (w.head >= p.heads[1]) {
+        w.head -= p.heads[1];
         w.which = 2;
       }
     }
-    w.head = h;
-    if (INTERLEAVED) {
-      w.ca = 2 * w.i;
-      w.cb = w.ca + 1;
-    } else if (w.i < fv) {
-      w.ca = w.i;
-      w.cb = w.i + fv;
-    } else {
-      w.ca = 2 * fv + 2 * (w.i - fv);
-      w.cb = w.ca + 1;
-    }
-    return w;
   };
+  Place first;
+  first.tau = pair0 / nh;
+  first.h = pair0 - first.tau * nh;
 
   V xa[ITEMS], xb[ITEMS];
+  {
+    Place w = first;
 #pragma unroll
-  for (int u = 0; u < ITEMS; ++u) {
-    const int it = tid + u * kRotThreads;
-    if (it < n_items) {
-      const Item w = locate(it);
+    for (int u = 0; u < ITEMS; ++u, w.h += STEP) {
+      if (pair0 + u * STEP >= n_pairs) break;
+      settle(w);
       const __nv_bfloat16* src = p.src[w.which] + (t0 + w.tau) * p.src_stride[w.which] + w.head * D;
-      xa[u] = *reinterpret_cast<const V*>(src + w.ca * VEC);
-      xb[u] = *reinterpret_cast<const V*>(src + w.cb * VEC);
+      xa[u] = *reinterpret_cast<const V*>(src + ca * VEC);
+      xb[u] = *reinterpret_cast<const V*>(src + cb * VEC);
     }
   }
 
@@ -220,11 +228,11 @@ __global__ void __launch_bounds__(kRotThreads) rotary_kernel(const RotaryParams 
     __syncthreads();
   }
 
+  Place w = first;
 #pragma unroll
-  for (int u = 0; u < ITEMS; ++u) {
-    const int it = tid + u * kRotThreads;
-    if (it >= n_items) continue;
-    const Item w = locate(it);
+  for (int u = 0; u < ITEMS; ++u, w.h += STEP) {
+    if (pair0 + u * STEP >= n_pairs) break;
+    settle(w);
     if (PAGED && !s_owned[w.tau]) continue;
     const uint32_t* wa = reinterpret_cast<const uint32_t*>(&xa[u]);
     const uint32_t* wb = reinterpret_cast<const uint32_t*>(&xb[u]);
@@ -236,9 +244,9 @@ __global__ void __launch_bounds__(kRotThreads) rotary_kernel(const RotaryParams 
       b[2 * i] = bf_lo(wb[i]);
       b[2 * i + 1] = bf_hi(wb[i]);
     }
-    if (w.which < 2 && w.i < fv) {
-      const float* cs = s_cos + w.tau * p.n_freq + w.i * VEC;
-      const float* sn = s_sin + w.tau * p.n_freq + w.i * VEC;
+    if (w.which < 2 && i < fv) {
+      const float* cs = s_cos + w.tau * p.n_freq + i * VEC;
+      const float* sn = s_sin + w.tau * p.n_freq + i * VEC;
       float c[VEC], s[VEC];
 #pragma unroll
       for (int i = 0; i < VEC / 4; ++i) {
@@ -266,20 +274,20 @@ __global__ void __launch_bounds__(kRotThreads) rotary_kernel(const RotaryParams 
     }
     if (!PAGED || w.which == 0) {
       __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.dst[w.which]) + (t0 + w.tau) * p.dst_stride[w.which] + w.head * D;
-      store_bf16<VEC>(dst + w.ca * VEC, a);
-      store_bf16<VEC>(dst + w.cb * VEC, b);
+      store_bf16<VEC>(dst + ca * VEC, a);
+      store_bf16<VEC>(dst + cb * VEC, b);
     } else {
       const long long slot = s_slot[w.tau];
       if (slot < 0) continue;
       const long long at = slot + w.head * p.head_stride;
       if constexpr (E4M3) {
         uint8_t* dst = static_cast<uint8_t*>(p.dst[w.which]) + at;
-        store_e4m3<VEC>(dst + w.ca * VEC, a, p.scale[w.which]);
-        store_e4m3<VEC>(dst + w.cb * VEC, b, p.scale[w.which]);
+        store_e4m3<VEC>(dst + ca * VEC, a, p.scale[w.which]);
+        store_e4m3<VEC>(dst + cb * VEC, b, p.scale[w.which]);
       } else {
         __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.dst[w.which]) + at;
-        store_bf16<VEC>(dst + w.ca * VEC, a);
-        store_bf16<VEC>(dst + w.cb * VEC, b);
+        store_bf16<VEC>(dst + ca * VEC, a);
+        store_bf16<VEC>(dst + cb * VEC, b);
       }
     }
   }
