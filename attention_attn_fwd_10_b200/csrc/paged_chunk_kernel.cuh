@@ -28,6 +28,11 @@
 // fp16 in shared memory (exactly) by four more warps, 12-15: 128 x D values a block, where splitting the weights as
 // well would take 256 x 128 and the time of the busiest warps (a block of two tiles, D = 64: 4.3k clk of softmax
 // instead of 2.1k).
+//
+// Measured (B200, the whole call on the device): 2048 new tokens at the end of 32768 keys, 32 heads over 8 of 128,
+// 1.07 TFLOP: 1000-1170 us as the power cap allows, 0.92-1.07 PFLOP/s (e4m3 cache: 1120-1150 us; the contiguous
+// forward of the same shape: 1008 us).  Bound, as that one, by the chain softmax -> P V -> S of a tile: 3.7k clk a
+// two-tile block, 1.05k of them MMAs.
 #pragma once
 
 #include <cuda_fp16.h>

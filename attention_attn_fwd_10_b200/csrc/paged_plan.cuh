@@ -3,12 +3,13 @@
 // Lengths are read when the call runs, so the host cannot lay the work out.  A
 // unit is up to `unit_pos` new tokens of one sequence and the query heads of
 // one kv head; its steps are the 128-key blocks its last token sees (one block
-// where it sees none: its rows still get their zeros), two steps a block where both
-// tiles work on it and one where the tokens fit one tile (a block of the chunk kernel takes 2.9 us for two
-// tiles, 1.2 us for one).  All units' steps form one
-// line, ordered by sequence, kv head, unit; CTA c takes the c-th of gridDim.x
-// equal stretches (units and stretches of an even length where a block may be two steps: no block is cut), so the loads are even whatever the lengths: a ragged batch, one long
-// sequence, chunks beside single tokens.  A unit cut by a stretch's end is
+// where it sees none: its rows still get their zeros), in the chunk kernel two steps a
+// block where both tiles work on it (2.2 to 2.3 us) and one where the tokens fit one
+// tile (1.0 to 1.2 us).  All units' steps form one line, ordered by sequence, kv head,
+// unit; CTA c takes the c-th of gridDim.x equal stretches (units and stretches have an
+// even length where a block may be two steps, so no block is cut).  So the loads are
+// even whatever the lengths: a ragged batch, one long sequence, chunks beside single
+// tokens.  A unit cut by a stretch's end is
 // computed in pieces, each left in the workspace as fp32 rows normalized over
 // the piece's keys with their log-sum-exp, and joined by paged_merge_kernel.
 // Every CTA finds its stretch by itself from the index arrays (two passes of 32
@@ -43,7 +44,7 @@ struct PagedParams {
   int min_steps;               // least steps of a CTA's stretch (likewise)
   float* o_part;               // [2 gridDim.x, unit_rows, D]
   float* l_part;               // [2 gridDim.x, unit_rows], base-2 log-sum-exp
-  int4* cut;                   // [2 gridDim.x]: the unit that stretch c starts inside of (CutUnit)
+  int4* cut;                   // [gridDim.x]: the unit that stretch c starts inside of (paged_cut)
   int* status;
   uint64_t wait_limit_ns;
 };
