@@ -47,20 +47,24 @@ struct FewLayout {
   static constexpr int Q_COL = NQ * ROW_BYTES;               // one box column of Q rows (e4m3: the hi or the lo rows)
   static constexpr int Q_BYTES = (KV8 ? 2 : NBOX) * Q_COL;
   static constexpr int P_BYTES = 2 * NQ * 128;               // bf16: two 64-key columns; e4m3: the hi and the lo terms
-  static constexpr int NBUF = 4;                             // score and P buffers in turn
+  static constexpr int NBUF = 4;                             // score buffers in turn
+  // P buffers and Q tiles in turn: fewer where that makes room for a third K and V tile (64 sequences of up to 8192
+  // bf16 keys, 8 tokens of 4 heads each: 215 us with two tiles, 195 with three)
+  static constexpr bool TIGHT = !KV8 && D == 128 && NQ == 32;
+  static constexpr int NPB = TIGHT ? 2 : 4, NQB = TIGHT ? 1 : 2;
   static constexpr int NS = KV8 ? 2 * NQ : NQ;               // MMA columns: e4m3: the hi terms, then the lo terms
   // as many tiles as shared memory holds
-  static constexpr int ROOM = 227 * 1024 - 1024 - 2 * Q_BYTES - NBUF * P_BYTES - 6 * 1024;
+  static constexpr int ROOM = 227 * 1024 - 1024 - NQB * Q_BYTES - NPB * P_BYTES - 5 * 1024;
   static constexpr int ST = ROOM / (2 * KV_BYTES) < 8 ? ROOM / (2 * KV_BYTES) : 8;
   static constexpr int K_OFF = 0;
   static constexpr int V_OFF = K_OFF + ST * KV_BYTES;
   static constexpr int P_OFF = V_OFF + ST * KV_BYTES;
-  static constexpr int Q_OFF = P_OFF + NBUF * P_BYTES;
-  static constexpr int BAR_OFF = Q_OFF + 2 * Q_BYTES;
+  static constexpr int Q_OFF = P_OFF + NPB * P_BYTES;
+  static constexpr int BAR_OFF = Q_OFF + NQB * Q_BYTES;
   static constexpr int NI = 4;
   static constexpr int B_Q_FULL = 0;                    // [NI] by piece: its Q, and the factors of its scores
-  static constexpr int B_Q_EMPTY = B_Q_FULL + NI;       // [2] by Q tile
-  static constexpr int B_K_FULL = B_Q_EMPTY + 2;        // [ST]
+  static constexpr int B_Q_EMPTY = B_Q_FULL + NI;       // [NQB] by Q tile
+  static constexpr int B_K_FULL = B_Q_EMPTY + NQB;      // [ST]
   static constexpr int B_K_EMPTY = B_K_FULL + ST;
   static constexpr int B_V_FULL = B_K_EMPTY + ST;
   static constexpr int B_V_EMPTY = B_V_FULL + ST;
@@ -105,33 +109,26 @@ constexpr float kNoKeyYet = -3e38f;  // a column's maximum before its first key
 
 template <int N>
 __device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, uint32_t* r) {
-  static_assert(N == 16 || N == 32 || N == 64, "columns");
+  static_assert(N == 16 || N == 32, "columns");
   if constexpr (N == 16) {
     tmem_ld16(taddr, r);
     tmem_ld_wait16(r);
-  } else if constexpr (N == 32) {
-    tmem_ld32(taddr, r);
-    tmem_ld_wait(r);
   } else {
     tmem_ld32(taddr, r);
-    tmem_ld32(taddr + 32, r + 32);
     tmem_ld_wait(r);
-    tmem_ld_wait(r + 32);
   }
 }
-// Multiplies a 32-lane accumulator's columns by per-column factors (e4m3: both terms' columns).
-template <int NQ, int NS>
-__device__ __forceinline__ void tmem_scale_cols(uint32_t taddr, const float* alpha) {
+// Multiplies an accumulator's NS columns, 16 at a time, by factors in shared memory (column c by alpha[c % nq]).
+template <int NS>
+__device__ __forceinline__ void tmem_scale_cols(uint32_t taddr, const float* alpha, int nq) {
+#pragma unroll 1
+  for (int x = 0; x < NS; x += 16) {
+    uint32_t r[16];
+    tmem_ld_cols<16>(taddr + x, r);
+    const float* a = alpha + (x >= nq ? x - nq : x);
 #pragma unroll
-  for (int x = 0; x < NS; x += NQ) {
-    uint32_t r[NQ];
-    tmem_ld_cols<NQ>(taddr + x, r);
-#pragma unroll
-    for (int q = 0; q < NQ; ++q) r[q] = __float_as_uint(__uint_as_float(r[q]) * alpha[q]);
-    if constexpr (NQ == 16)
-      tmem_st16(taddr + x, r);
-    else
-      tmem_st32(taddr + x, r);
+    for (int q = 0; q < 16; ++q) r[q] = __float_as_uint(__uint_as_float(r[q]) * a[q]);
+    tmem_st16(taddr + x, r);
   }
   tmem_st_wait();
 }
@@ -209,7 +206,7 @@ __global__ void __launch_bounds__(FewLayout<D, KV8, NQ>::THREADS, 1)
     tma_prefetch_desc(&tm_v);
   }
   // Q rows that no load reaches stay zero (padding columns of the products)
-  for (int i = threadIdx.x; i < 2 * L::Q_BYTES / 16; i += 256)
+  for (int i = threadIdx.x; i < L::NQB * L::Q_BYTES / 16; i += 256)
     if (warp < 8) *reinterpret_cast<uint4*>(sptr + L::Q_OFF + i * 16) = make_uint4(0, 0, 0, 0);
   if (threadIdx.x < NQ) reinterpret_cast<int*>(sptr + L::POS_OFF)[threadIdx.x] = static_cast<int>(threadIdx.x) / p.group;
   PagedWalk walk;
@@ -248,8 +245,9 @@ __global__ void __launch_bounds__(FewLayout<D, KV8, NQ>::THREADS, 1)
         continue;
       }
       if constexpr (!KV8) {
-        const int qs = qn & 1;
-        if (qn >= 2 && !(ok = __all_sync(0xffffffffu, mbar_wait(bar(L::B_Q_EMPTY + qs), ((qn >> 1) - 1) & 1, ctl)))) break;
+        const int qs = qn % L::NQB;
+        if (qn >= L::NQB && !(ok = __all_sync(0xffffffffu, mbar_wait(bar(L::B_Q_EMPTY + qs), (qn / L::NQB - 1) & 1, ctl))))
+          break;
         if (lane == 0) {
           mbar_arrive_expect_tx(bar(L::B_Q_FULL + u % L::NI), L::NBOX * p.group * p.tile_pos * 128);
 #pragma unroll
@@ -302,14 +300,14 @@ __global__ void __launch_bounds__(FewLayout<D, KV8, NQ>::THREADS, 1)
         for (int j = 0; j < n; ++j, ++g) {
           const int buf = g % L::NBUF, stage = g % L::ST;
           ok = mbar_wait(bar(L::B_K_FULL + stage), (g / L::ST) & 1, ctl);
-          // four blocks ago: the scores were read before P was published, and P V is complete, so the softmax
-          // that S_FULL wakes finds its P buffer free
+          // four blocks ago: the scores were read before P was published, and P V is complete, so (with four P buffers)
+          // the softmax that S_FULL wakes finds its P buffer free
           if (ok && g >= L::NBUF) ok = mbar_wait(bar(L::B_PV_DONE + buf), ((g / L::NBUF) - 1) & 1, ctl);
           if (ok && j == 0) ok = mbar_wait(bar(L::B_Q_FULL + u % L::NI), (u / L::NI) & 1, ctl);
           if (!ok) break;
           tc_fence_after();
           const uint32_t kd = sdesc_lo(sbase + L::K_OFF + stage * L::KV_BYTES, 16);
-          const uint32_t qd = sdesc_lo(sbase + L::Q_OFF + (qi & 1) * L::Q_BYTES, 16);
+          const uint32_t qd = sdesc_lo(sbase + L::Q_OFF + (qi % L::NQB) * L::Q_BYTES, 16);
           if constexpr (KV8) {
 #pragma unroll
             for (int kk = 0; kk < D / 32; ++kk)
@@ -325,7 +323,7 @@ __global__ void __launch_bounds__(FewLayout<D, KV8, NQ>::THREADS, 1)
           umma_commit(bar(L::B_S_FULL + buf));
           umma_commit(bar(L::B_K_EMPTY + stage));
           if (j == n - 1) {
-            umma_commit(bar(L::B_Q_EMPTY + (qi & 1)));
+            umma_commit(bar(L::B_Q_EMPTY + qi % L::NQB));
             ++qi;
           }
         }
@@ -355,7 +353,7 @@ __global__ void __launch_bounds__(FewLayout<D, KV8, NQ>::THREADS, 1)
         if (lane == 0) {
           tc_fence_after();
           const uint32_t od = tmem + L::o_col(g & 1);
-          const uint32_t pd = sdesc_lo(sbase + L::P_OFF + buf * L::P_BYTES, 16);
+          const uint32_t pd = sdesc_lo(sbase + L::P_OFF + g % L::NPB * L::P_BYTES, 16);
           if constexpr (KV8) {
             const uint32_t vd = sdesc_lo(sbase + L::V_OFF + stage * L::KV_BYTES, 16);
 #pragma unroll
@@ -409,8 +407,8 @@ __global__ void __launch_bounds__(FewLayout<D, KV8, NQ>::THREADS, 1)
       if constexpr (KV8) {
         if (it.n_loads > 0) {
           for (; j < it.n_loads && vn < L::ST; ++j) load_v();  // (the first blocks, while the ring is empty)
-          const int qs = qn & 1;
-          if (qn >= 2 && !__all_sync(0xffffffffu, mbar_wait(bar(L::B_Q_EMPTY + qs), ((qn >> 1) - 1) & 1, ctl))) break;
+          const int qs = qn % L::NQB;
+          if (qn >= L::NQB && !__all_sync(0xffffffffu, mbar_wait(bar(L::B_Q_EMPTY + qs), (qn / L::NQB - 1) & 1, ctl))) break;
           ++qn;
           // 16 dims of a row per lane, D / 16 lanes side by side on a row; a loop, not unrolled: this runs once or
           // twice per CTA, and fetching its instructions is what it costs (unrolled over a whole row: 10k clk)
@@ -499,19 +497,28 @@ __global__ void __launch_bounds__(FewLayout<D, KV8, NQ>::THREADS, 1)
       }
       if (KV8 && nb > 0) wait_for(L::B_Q_FULL + u % L::NI, u / L::NI);  // (the factors of the scores)
       // (the last piece's maxima were read before the vote above)
-      if ((threadIdx.x & 127) < NQ) moved[threadIdx.x & 127] = kNoKeyYet;
+      if ((threadIdx.x & 127) < NQ) {
+        const int q = threadIdx.x & 127;
+        moved[q] = q < real ? kNoKeyYet : -kNoKeyYet;
+        moved[NQ + q] = 1.f;
+      }
       bool first = true;  // no block of this stream yet
       for (int gg = g; gg < g + nb; ++gg) {
         if ((gg & 1) != t) continue;
         const int buf = gg % L::NBUF;
         wait_for(L::B_S_FULL + buf, gg / L::NBUF);
         tc_fence_after();
-        uint32_t sr[L::NS];
-        tmem_ld_cols<L::NS>(tmem + lane_addr + L::s_col(buf), sr);
+        uint32_t sr[NQ];
+        tmem_ld_cols<NQ>(tmem + lane_addr + L::s_col(buf), sr);
         float* s = reinterpret_cast<float*>(sr);
         if constexpr (KV8) {
 #pragma unroll
-          for (int q = 0; q < NQ; ++q) s[q] = fmaf(s[NQ + q], L::LO, s[q]);
+          for (int x = 0; x < NQ; x += 16) {
+            uint32_t lo[16];
+            tmem_ld_cols<16>(tmem + lane_addr + L::s_col(buf) + NQ + x, lo);
+#pragma unroll
+            for (int q = 0; q < 16; ++q) s[x + q] = fmaf(__uint_as_float(lo[q]), L::LO, s[x + q]);
+          }
         }
         // scores in base-2 units
         if constexpr (KV8) {
@@ -558,21 +565,20 @@ __global__ void __launch_bounds__(FewLayout<D, KV8, NQ>::THREADS, 1)
             moved[NQ + q] = moves ? exp2_mufu(old - to) : 1.f;
           }
           group_sync(1 + t);
-          float alpha[NQ];
 #pragma unroll
           for (int q = 0; q < NQ; ++q) {
-            if (q < real) m[q] = moved[q];
-            alpha[q] = q < real ? moved[NQ + q] : 1.f;
-            l[q] *= alpha[q];
+            m[q] = moved[q];
+            l[q] *= moved[NQ + q];
           }
           if (!first) {
             // the stream's earlier P V must be complete before its accumulator is scaled
             wait_for(L::B_PV_DONE + (gg - 2) % L::NBUF, (gg - 2) / L::NBUF);
             tc_fence_after();
-            tmem_scale_cols<NQ, L::NS>(tmem + lane_addr + L::o_col(t), alpha);
+            tmem_scale_cols<L::NS>(tmem + lane_addr + L::o_col(t), moved + NQ, NQ);
           }
         }
-        uint8_t* const pb = sptr + L::P_OFF + buf * L::P_BYTES + p_at;
+        if (L::NPB == 2 && gg >= 2) wait_for(L::B_PV_DONE + (gg - 2) % L::NBUF, (gg - 2) / L::NBUF);  // its P is read
+        uint8_t* const pb = sptr + L::P_OFF + gg % L::NPB * L::P_BYTES + p_at;
 #pragma unroll
         for (int q = 0; q < NQ; q += 2) {
           const float e0 = exp2_mufu(s[q] - m[q]), e1 = exp2_mufu(s[q + 1] - m[q + 1]);
