@@ -668,6 +668,7 @@ __global__ void __launch_bounds__(ChunkLayout<D, KV8>::THREADS, 1)
           const size_t part = static_cast<size_t>(max(slot, 0)) * p.unit_rows + t * 128 + row;
 #pragma unroll 1
           for (int ch = 0; ch < D / 16; ++ch) {
+            __syncwarp();  // the tensor-memory loads take the whole warp, the stores below only real rows
             uint32_t orr[16], obr[16];
             if (nb > 0) {
               tmem_ld16(oa_addr + ch * 16, orr);

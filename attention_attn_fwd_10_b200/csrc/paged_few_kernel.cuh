@@ -668,6 +668,7 @@ __global__ void __launch_bounds__(FewLayout<D, KV8, NQ>::THREADS, 1)
         long long at = slot >= 0 ? static_cast<long long>(part) * D + d : (row0 * p.H_q + head0) * D + d;
 #pragma unroll 1
         for (int c0 = 0; c0 < real; c0 += 16) {  // 16 columns at a time
+          __syncwarp();  // the tensor-memory loads take the whole warp, the stores below not every lane
           float x[16];
 #pragma unroll
           for (int q = 0; q < 16; ++q) x[q] = 0.f;
