@@ -586,3 +586,22 @@ def test_refusals():
     with pytest.raises(ValueError):
         attn.paged_append(c, k, torch.zeros((2, 2, 64), dtype=torch.bfloat16, device="cuda"))
     assert attn.device_status() == 0
+
+
+@pytest.mark.parametrize("max_new", [1, 300])
+def test_lse_keeps_32_bits(max_new):
+    """Rows that few keys dominate: the row's sum is as exact as its largest weights.  Bounds: a score is D / 16 partial
+    sums and one across them, each cut at 2^-23 of at most sum |q k| scale, twice for the sums inside one; the row's
+    sum 25 roundings of 2^-24, ex2 2^-22; exponent, maximum and scale 2^-24 of the largest score each, the result twice."""
+    D, scale = 64, 64 ** -0.5
+    x = make([max_new, 1], [700, 900], 8, 2, D, 64, q_gain=3.0, seed=41)
+    _, lse, want = _attend(x, False, max_new=max_new)
+    most = 0.0
+    for b in range(2):
+        k = np.abs(oracle.gather(x["k_cache"], x["page_table"].numpy()[b], x["keys"][b]))  # [keys, H_kv, D]
+        q = np.abs(x["q"][x["start"][b]:x["start"][b + 1]].double().numpy())
+        for h in range(8):
+            most = max(most, float((q[:, h] @ k[:, h // 4].T).max()) * scale)
+    bound = 2 * (D / 16 + 1) * 2.0 ** -23 * most + 25 * 2.0 ** -24 + 2.0 ** -22 + 5 * 2.0 ** -24 * most
+    err = np.abs(parity.to_np(lse) - want[1])
+    assert err.max() <= bound, f"lse {err.max():.3e} > {bound:.3e}"
