@@ -158,7 +158,7 @@ __device__ __forceinline__ float exp_weights(const uint32_t* sr, float c, float 
     const float e0 = exp2_mufu(x0), e1 = exp2_mufu(x1);
     acc[q & 3] = f2_add(acc[q & 3], f2_pack(e0, e1));
     if constexpr (F16)
-      asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(pk[q]) : "f"(e1), "f"(e0));
+      pk[q] = pack_f16x2(e0, e1);
     else
       pk[q] = pack_bf16x2(e0, e1);
   }
@@ -495,30 +495,7 @@ __global__ void __launch_bounds__(ChunkLayout<D, KV8>::THREADS, 1)
         if (ok && n >= L::VMST) ok = mbar_wait(bar(L::B_VM_EMPTY + sm), ((n / L::VMST) - 1) & 1, ctl);
         if (!(ok = __all_sync(0xffffffffu, ok))) break;
         const int live = len - (j0 + j) * L::BN;  // rows past the sequence's end become zeros
-        const uint8_t* src = sptr + L::V_OFF + s * L::KV_BYTES;
-        uint8_t* dst = sptr + L::VM_OFF + sm * L::VM_BYTES;
-        // 16 dims of a key at a time: a 16-byte chunk in, two out
-        constexpr int CHUNKS = D / 16;
-#pragma unroll
-        for (int i = 0; i < CHUNKS; ++i) {
-          const int e = i * 128 + tid, key = e / CHUNKS, c = e % CHUNKS;
-          const int sw = L::ROW_BYTES == 128 ? (key & 7) : ((key >> 1) & 3);
-          const uint4 x = *reinterpret_cast<const uint4*>(src + key * L::ROW_BYTES + ((c ^ sw) * 16));
-          const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-          uint32_t y[8];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(y[2 * k]) : "h"(static_cast<uint16_t>(w[k])));
-            asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(y[2 * k + 1]) : "h"(static_cast<uint16_t>(w[k] >> 16)));
-          }
-          const bool in = key < live;
-          uint8_t* row = dst + (c >> 2) * (128 * 128) + key * 128;
-          *reinterpret_cast<uint4*>(row + (((2 * c) & 7) ^ (key & 7)) * 16) =
-              in ? make_uint4(y[0], y[1], y[2], y[3]) : make_uint4(0, 0, 0, 0);
-          *reinterpret_cast<uint4*>(row + (((2 * c + 1) & 7) ^ (key & 7)) * 16) =
-              in ? make_uint4(y[4], y[5], y[6], y[7]) : make_uint4(0, 0, 0, 0);
-        }
-        fence_proxy_async_smem();
+        convert_block<D>(sptr + L::V_OFF + s * L::KV_BYTES, sptr + L::VM_OFF + sm * L::VM_BYTES, live, tid);
         mbar_arrive_warp(bar(L::B_VM_FULL + sm));
         mbar_arrive_warp(bar(L::B_V_EMPTY + s));
       }

@@ -8,22 +8,29 @@
 // A softmax thread owns a key: it has NQ scores to exponentiate instead of 128, so the
 // chain of a block is a few hundred clocks and the kernel runs at the rate of its loads.
 // The running maximum of a column runs across threads; it moves only where a weight would exceed
-// 2^(SHIFT + TAU) = 2^8, which one barrier with an OR over the warpgroup tells.  Row sums stay per
+// 2^(SHIFT + TAU), which one barrier with an OR over the warpgroup tells.  Row sums stay per
 // thread until the piece ends.  Warps:
 //   0-3, 4-7  softmax of the even and the odd blocks (two streams with statistics and
 //             accumulator of their own, joined at the piece's end by the first)
 //   8         TMA producer of Q (bf16 cache), of K, and of V where a block is few boxes
 //   9         tensor memory; issues the S MMAs, up to four blocks ahead of P V, across pieces
-//   10        issues the P V MMAs (and writes zeros over V's rows past a sequence's end)
+//   10        issues the P V MMAs (bf16 cache: writes zeros over V's rows past a sequence's end first)
 //   11        scheduler; e4m3 cache: writes Q as two e4m3 terms; pages of less than 64 keys: TMA producer of V
-// P^T goes to shared memory (the B operand's place), four buffers in turn.
+//   12-15     e4m3 cache: V from e4m3 to fp16
+// P^T goes to shared memory (the B operand's place), four buffers in turn (two where NQ = 32 and D = 128).
+// The weights are rounded to the 16 bits of V's MMA, bf16 or fp16, as the forward rounds them; the row sums add
+// the fp32 values.
 //
 // An MMA of M = 128 and N <= 32 takes 46 clk whatever N is (65 at N = 128), and issuing one about as long: with
-// one issuing thread for both products a block took 1800 clk.  e4m3 cache: q and the weights are sums of two
+// one issuing thread for both products a block took 1800 clk.  e4m3 cache: q is a sum of two
 // e4m3 terms (x = hi + lo, hi = e4m3(x), lo = e4m3(x - hi): 8 bits of x), which stand side by side as 2 NQ columns
-// of the same MMAs -- half the MMAs of two passes -- and are added in the softmax and in the epilogue.  The low
-// terms carry a factor of 16, so a weight's floor is 2^-14: with a row's largest weight at 2^SHIFT or more, 2^-17
-// of it.
+// of the same MMAs -- half the MMAs of two passes -- and are added in the softmax (the low terms carry a factor of 16).
+// The weights are fp16 and V is turned into fp16, exactly, by four more warps.  Two e4m3 terms per weight would end at
+// 2^-17 of a row's largest: 32768 keys of 2^-17 each are a quarter of it, and with one key 12 nats above the others O
+// was 12 % off.  Sixteen warps of six roles fill the instruction cache: what is kept small for that (one copy of the
+// loading code for K and V, a rolled conversion, paged_wait, issuers elected so that descriptors stay uniform) took
+// 64 sequences of up to 4096 e4m3 keys from 117 to 78 us, and the stalls for want of an instruction from 4.9 to 1.7 per
+// instruction issued.
 //
 // Measured (B200, the whole call on the device): 64 sequences of up to 8192 bf16 keys, 8 kv heads of 128, 1.12 GB:
 // 173-179 us, 6.3-6.5 TB/s, bound by DRAM.  4 x 32768 e4m3 keys, 268 MB: 57-61 us, 4.4-4.7 TB/s: 43 us of loads at
@@ -46,19 +53,24 @@ struct FewLayout {
   static constexpr int KV_BYTES = NBOX * BOX_BYTES;
   static constexpr int Q_COL = NQ * ROW_BYTES;               // one box column of Q rows (e4m3: the hi or the lo rows)
   static constexpr int Q_BYTES = (KV8 ? 2 : NBOX) * Q_COL;
-  static constexpr int P_BYTES = 2 * NQ * 128;               // bf16: two 64-key columns; e4m3: the hi and the lo terms
+  static constexpr int P_BYTES = 2 * NQ * 128;               // two 64-key columns of bf16 (e4m3 cache: of fp16)
+  // V as the MMA reads it: D / 64 columns of 128-byte rows of 16-bit values (e4m3: written by the converters)
+  static constexpr int VM_COL = 128 * 128;
+  static constexpr int VM_BYTES = 128 * D * 2;
+  static constexpr int VMST = KV8 ? 2 : 0;
   static constexpr int NBUF = 4;                             // score buffers in turn
-  // P buffers and Q tiles in turn: fewer where that makes room for a third K and V tile (64 sequences of up to 8192
+  // P buffers and Q tiles in turn: fewer where that makes room for another K and V tile (64 sequences of up to 8192
   // bf16 keys, 8 tokens of 4 heads each: 215 us with two tiles, 195 with three)
-  static constexpr bool TIGHT = !KV8 && D == 128 && NQ == 32;
+  static constexpr bool TIGHT = D == 128 && NQ == 32;
   static constexpr int NPB = TIGHT ? 2 : 4, NQB = TIGHT ? 1 : 2;
-  static constexpr int NS = KV8 ? 2 * NQ : NQ;               // MMA columns: e4m3: the hi terms, then the lo terms
+  static constexpr int NS = KV8 ? 2 * NQ : NQ;               // columns of S^T: e4m3: q's hi terms, then its lo terms
   // as many tiles as shared memory holds
-  static constexpr int ROOM = 227 * 1024 - 1024 - NQB * Q_BYTES - NPB * P_BYTES - 5 * 1024;
+  static constexpr int ROOM = 227 * 1024 - 1024 - NQB * Q_BYTES - NPB * P_BYTES - VMST * VM_BYTES - 5 * 1024;
   static constexpr int ST = ROOM / (2 * KV_BYTES) < 8 ? ROOM / (2 * KV_BYTES) : 8;
   static constexpr int K_OFF = 0;
   static constexpr int V_OFF = K_OFF + ST * KV_BYTES;
-  static constexpr int P_OFF = V_OFF + ST * KV_BYTES;
+  static constexpr int VM_OFF = V_OFF + ST * KV_BYTES;
+  static constexpr int P_OFF = VM_OFF + VMST * VM_BYTES;
   static constexpr int Q_OFF = P_OFF + NPB * P_BYTES;
   static constexpr int BAR_OFF = Q_OFF + NQB * Q_BYTES;
   static constexpr int NI = 4;
@@ -68,7 +80,8 @@ struct FewLayout {
   static constexpr int B_K_EMPTY = B_K_FULL + ST;
   static constexpr int B_V_FULL = B_K_EMPTY + ST;
   static constexpr int B_V_EMPTY = B_V_FULL + ST;
-  static constexpr int B_S_FULL = B_V_EMPTY + ST;       // [NBUF]
+  static constexpr int B_VM_FULL = B_V_EMPTY + ST;      // [VMST] e4m3: converted (four warps)
+  static constexpr int B_S_FULL = B_VM_FULL + VMST;     // [NBUF]
   static constexpr int B_P_FULL = B_S_FULL + NBUF;      // [NBUF] four warps
   static constexpr int B_PV_DONE = B_P_FULL + NBUF;     // [NBUF]
   static constexpr int B_O_FINAL = B_PV_DONE + NBUF;
@@ -78,7 +91,7 @@ struct FewLayout {
   static constexpr int B_ITEM_EMPTY = B_ITEM_FULL + NI;
   static constexpr int B_DRAIN = B_ITEM_EMPTY + NI;
   static constexpr int N_BARS = B_DRAIN + 2;
-  static constexpr int ITEM_READERS = 11;  // 8 softmax warps, K's producer, the two issuers
+  static constexpr int ITEM_READERS = KV8 ? 15 : 11;  // 8 softmax warps, K's producer, the two issuers, 4 converters
   static constexpr int ITEM_OFF = BAR_OFF + (8 * N_BARS + 15) / 16 * 16;
   static constexpr int CQ_OFF = ITEM_OFF + NI * static_cast<int>(sizeof(PagedItem));  // [NI][NQ] factors of the scores
   static constexpr int STAT_OFF = CQ_OFF + NI * NQ * 4;    // [2 streams][5][NQ]: four warps' sums, the maximum
@@ -93,14 +106,19 @@ struct FewLayout {
   static_assert(SMEM_BYTES <= 232448, "shared memory budget");
   static_assert(Q_COL % 1024 == 0 && P_BYTES % 2048 == 0, "operand tiles on swizzle boundaries");
   __device__ static constexpr uint32_t s_col(int b) { return static_cast<uint32_t>(b) * NS; }
-  __device__ static constexpr uint32_t o_col(int t) { return static_cast<uint32_t>(NBUF + t) * NS; }
+  __device__ static constexpr uint32_t o_col(int t) { return static_cast<uint32_t>(NBUF * NS + t * NQ); }
   static constexpr uint32_t TMEM_COLS = NS == 16 ? 128 : (NS == 32 ? 256 : 512);
-  static constexpr int THREADS = 384;
+  static_assert(NBUF * NS + 2 * NQ <= static_cast<int>(TMEM_COLS), "tensor memory columns");
+  static constexpr int THREADS = KV8 ? 512 : 384;
+  // e4m3: 2 x 128 x 168 + 2 x 128 x 88 = 512 x 128
+  static constexpr int REG_LAUNCH = 128, REG_SOFTMAX = 168, REG_OTHER = 88;
   static constexpr int WARP_K = 8, WARP_S = 9, WARP_PV = 10, WARP_SCHED = 11;
-  // weights up to 2^(SHIFT + TAU) = 2^8; a column's largest at 2^SHIFT or more
-  static constexpr float SHIFT = KV8 ? 3.f : 0.f;
-  static constexpr float TAU = KV8 ? 5.f : 8.f;
-  static constexpr float LO = 1.f / 16.f;  // e4m3: what a lo term stands for
+  // Weights up to 2^(SHIFT + TAU); a column's largest at 2^SHIFT or more.  bf16 weights have fp32's range.  fp16's end
+  // at 65504, and below 2^-14 they step by 2^-24: with the largest at 2^7 to 2^15 a small weight is off by at most
+  // 2^-32 of the largest (a row of 32768 keys by 2^-17 of it).
+  static constexpr float SHIFT = KV8 ? 7.f : 0.f;
+  static constexpr float TAU = 8.f;
+  static constexpr float LO = 1.f / 16.f;  // e4m3: what q's lo term stands for
   static constexpr uint32_t HI = ROW_BYTES == 128 ? sdesc_sw128_hi(1024) : sdesc_sw64_hi(512);
   static constexpr uint32_t HI128 = sdesc_sw128_hi(1024);
 };
@@ -118,16 +136,15 @@ __device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, uint32_t* r) {
     tmem_ld_wait(r);
   }
 }
-// Multiplies an accumulator's NS columns, 16 at a time, by factors in shared memory (column c by alpha[c % nq]).
-template <int NS>
-__device__ __forceinline__ void tmem_scale_cols(uint32_t taddr, const float* alpha, int nq) {
+// Multiplies an accumulator's N columns, 16 at a time, by factors in shared memory.
+template <int N>
+__device__ __forceinline__ void tmem_scale_cols(uint32_t taddr, const float* alpha) {
 #pragma unroll 1
-  for (int x = 0; x < NS; x += 16) {
+  for (int x = 0; x < N; x += 16) {
     uint32_t r[16];
     tmem_ld_cols<16>(taddr + x, r);
-    const float* a = alpha + (x >= nq ? x - nq : x);
 #pragma unroll
-    for (int q = 0; q < 16; ++q) r[q] = __float_as_uint(__uint_as_float(r[q]) * a[q]);
+    for (int q = 0; q < 16; ++q) r[q] = __float_as_uint(__uint_as_float(r[q]) * alpha[x + q]);
     tmem_st16(taddr + x, r);
   }
   tmem_st_wait();
@@ -190,6 +207,8 @@ __global__ void __launch_bounds__(FewLayout<D, KV8, NQ>::THREADS, 1)
     for (int i = 0; i < L::N_BARS; ++i) {
       uint32_t n = 1;
       if ((i >= L::B_P_FULL && i < L::B_P_FULL + L::NBUF) || i == L::B_XCHG || i == L::B_XCHG_READ) n = 4;
+      if (KV8 && i >= L::B_V_EMPTY && i < L::B_V_EMPTY + L::ST) n = 4;  // read by the converters
+      if (KV8 && i >= L::B_VM_FULL && i < L::B_VM_FULL + L::VMST) n = 4;
       if (i >= L::B_ITEM_EMPTY && i < L::B_ITEM_EMPTY + L::NI) n = L::ITEM_READERS;
       mbar_init(bar(i), n);
     }
@@ -223,12 +242,16 @@ __global__ void __launch_bounds__(FewLayout<D, KV8, NQ>::THREADS, 1)
   auto item_at = [&](int u) -> const volatile PagedItem* {
     return reinterpret_cast<const volatile PagedItem*>(sptr + L::ITEM_OFF + (u % L::NI) * sizeof(PagedItem));
   };
-  auto wait_item = [&](int u) { return mbar_wait(bar(L::B_ITEM_FULL + u % L::NI), (u / L::NI) & 1, ctl); };
+  auto wait_item = [&](int u) { return paged_wait(bar(L::B_ITEM_FULL + u % L::NI), (u / L::NI) & 1, ctl); };
   auto item_done = [&](int u) { return bar(L::B_ITEM_EMPTY + u % L::NI); };
   // One warp loads K and V in turn, unless a tile is many boxes (a warp issues one in about 100 clk): 4 x 32768 e4m3
   // keys in pages of 128 took 59 us with one warp and 63 with two, 64 sequences in pages of 16 211 and 176.
   const bool one_loader = p.box_shift >= 6;
 
+  if constexpr (KV8) {
+    static_assert(256 * L::REG_SOFTMAX + (L::THREADS - 256) * L::REG_OTHER <= L::THREADS * L::REG_LAUNCH, "register split");
+    if (warp >= 8) setmaxnreg_dec<L::REG_OTHER>();
+  }
   if (warp == L::WARP_K) {
     // ===================== TMA producer: Q, K =====================
     int kn = 0, vn = 0, qn = 0;
@@ -246,7 +269,7 @@ __global__ void __launch_bounds__(FewLayout<D, KV8, NQ>::THREADS, 1)
       }
       if constexpr (!KV8) {
         const int qs = qn % L::NQB;
-        if (qn >= L::NQB && !(ok = __all_sync(0xffffffffu, mbar_wait(bar(L::B_Q_EMPTY + qs), (qn / L::NQB - 1) & 1, ctl))))
+        if (qn >= L::NQB && !(ok = __all_sync(0xffffffffu, paged_wait(bar(L::B_Q_EMPTY + qs), (qn / L::NQB - 1) & 1, ctl))))
           break;
         if (lane == 0) {
           mbar_arrive_expect_tx(bar(L::B_Q_FULL + u % L::NI), L::NBOX * p.group * p.tile_pos * 128);
@@ -263,15 +286,14 @@ __global__ void __launch_bounds__(FewLayout<D, KV8, NQ>::THREADS, 1)
       for (int j = 0; ok && j < n_loads; ++j) {
         const int s = kn % L::ST;
         const uint32_t ph = ((kn / L::ST) - 1) & 1;
-        if (kn >= L::ST && !(ok = __all_sync(0xffffffffu, mbar_wait(bar(L::B_K_EMPTY + s), ph, ctl)))) break;
-        load_block<L::NBOX, L::ROW_BYTES>(p, &tm_k, sbase + L::K_OFF + s * L::KV_BYTES, bar(L::B_K_FULL + s), win, seq, head,
-                                          len, j0 + j, lane);
-        ++kn;
-        if (!one_loader) continue;
-        if (vn >= L::ST && !(ok = __all_sync(0xffffffffu, mbar_wait(bar(L::B_V_EMPTY + s), ph, ctl)))) break;
-        load_block<L::NBOX, L::ROW_BYTES>(p, &tm_v, sbase + L::V_OFF + s * L::KV_BYTES, bar(L::B_V_FULL + s), win, seq, head,
-                                          len, j0 + j, lane);
-        ++vn;
+        if (kn >= L::ST && !(ok = __all_sync(0xffffffffu, paged_wait(bar(L::B_K_EMPTY + s), ph, ctl)))) break;
+#pragma unroll 1  // (one copy of the code)
+        for (int v = 0; v < (one_loader ? 2 : 1); ++v) {
+          if (v == 1 && vn >= L::ST && !(ok = __all_sync(0xffffffffu, paged_wait(bar(L::B_V_EMPTY + s), ph, ctl)))) break;
+          load_block<L::NBOX, L::ROW_BYTES>(p, v == 0 ? &tm_k : &tm_v, sbase + (v == 0 ? L::K_OFF : L::V_OFF) + s * L::KV_BYTES,
+                                            bar((v == 0 ? L::B_K_FULL : L::B_V_FULL) + s), win, seq, head, len, j0 + j, lane);
+          ++(v == 0 ? kn : vn);
+        }
       }
     }
     // Drain: every load this warp issued has landed before the CTA may exit.
@@ -287,7 +309,7 @@ __global__ void __launch_bounds__(FewLayout<D, KV8, NQ>::THREADS, 1)
     }
   } else if (warp == L::WARP_S) {
     // ===================== S^T = K Q^T =====================
-    if (lane == 0) {
+    if (elect_one()) {
       constexpr uint32_t IDESC = KV8 ? idesc_e4m3_f32(128, L::NS) : idesc_bf16_f32(128, L::NS, false, false);
       int g = 0, qi = 0;
       bool ok = true;
@@ -299,11 +321,11 @@ __global__ void __launch_bounds__(FewLayout<D, KV8, NQ>::THREADS, 1)
         if (row0 < 0) break;
         for (int j = 0; j < n; ++j, ++g) {
           const int buf = g % L::NBUF, stage = g % L::ST;
-          ok = mbar_wait(bar(L::B_K_FULL + stage), (g / L::ST) & 1, ctl);
+          ok = paged_wait(bar(L::B_K_FULL + stage), (g / L::ST) & 1, ctl);
           // four blocks ago: the scores were read before P was published, and P V is complete, so (with four P buffers)
           // the softmax that S_FULL wakes finds its P buffer free
-          if (ok && g >= L::NBUF) ok = mbar_wait(bar(L::B_PV_DONE + buf), ((g / L::NBUF) - 1) & 1, ctl);
-          if (ok && j == 0) ok = mbar_wait(bar(L::B_Q_FULL + u % L::NI), (u / L::NI) & 1, ctl);
+          if (ok && g >= L::NBUF) ok = paged_wait(bar(L::B_PV_DONE + buf), ((g / L::NBUF) - 1) & 1, ctl);
+          if (ok && j == 0) ok = paged_wait(bar(L::B_Q_FULL + u % L::NI), (u / L::NI) & 1, ctl);
           if (!ok) break;
           tc_fence_after();
           const uint32_t kd = sdesc_lo(sbase + L::K_OFF + stage * L::KV_BYTES, 16);
@@ -333,48 +355,46 @@ __global__ void __launch_bounds__(FewLayout<D, KV8, NQ>::THREADS, 1)
     }
   } else if (warp == L::WARP_PV) {
     // ===================== O^T += V^T P^T =====================
-    constexpr uint32_t IDESC = KV8 ? (idesc_e4m3_f32(D, L::NS) | (1u << 15)) : idesc_bf16_f32(D, L::NS, true, false);
+    // (bf16's type codes are 1, fp16's 0)
+    constexpr uint32_t IDESC = idesc_bf16_f32(D, NQ, true, false) & ~(KV8 ? (1u << 7) | (1u << 10) : 0u);
+    // V as the MMAs read it: loaded (bf16), converted (e4m3)
+    constexpr int V_READY = KV8 ? L::B_VM_FULL : L::B_V_FULL, V_STAGES = KV8 ? L::VMST : L::ST;
+    constexpr int V_PLACE = KV8 ? L::VM_OFF : L::V_OFF;
+    // bf16: the whole warp, which may have zeros to write; e4m3: one lane
+    auto all = [](bool x) { return KV8 ? x : __all_sync(0xffffffffu, x) != 0; };
     int g = 0;
-    bool ok = true;
+    const bool issuer = KV8 ? elect_one() : lane == 0;
+    bool ok = !KV8 || issuer;
     for (int u = 0; ok; ++u) {
-      if (!(ok = __all_sync(0xffffffffu, wait_item(u)))) break;
+      if (!(ok = all(wait_item(u)))) break;
       const volatile PagedItem* it = item_at(u);
       const int row0 = it->row0, n = it->n_loads, len = it->len, j0 = it->j0;
-      mbar_arrive_warp(item_done(u));
+      if (!KV8) __syncwarp();
+      if (issuer) mbar_arrive(item_done(u));
       if (row0 < 0) break;
       for (int j = 0; j < n; ++j, ++g) {
-        const int buf = g % L::NBUF, stage = g % L::ST;
-        ok = mbar_wait(bar(L::B_V_FULL + stage), (g / L::ST) & 1, ctl);
-        if (!(ok = __all_sync(0xffffffffu, ok))) break;
+        const int buf = g % L::NBUF, stage = g % V_STAGES;
+        if (!(ok = all(paged_wait(bar(V_READY + stage), (g / V_STAGES) & 1, ctl)))) break;
         const int live = len - (j0 + j) * L::BN;  // keys of the block that the sequence has
-        if (live < L::BN) zero_tail<L::NBOX, L::ROW_BYTES>(sptr + L::V_OFF + stage * L::KV_BYTES, live, lane);
-        ok = mbar_wait(bar(L::B_P_FULL + buf), (g / L::NBUF) & 1, ctl);
-        if (!(ok = __all_sync(0xffffffffu, ok))) break;
-        if (lane == 0) {
+        if (!KV8 && live < L::BN) zero_tail<L::NBOX, L::ROW_BYTES>(sptr + V_PLACE + stage * L::VM_BYTES, live, lane);
+        if (!(ok = all(paged_wait(bar(L::B_P_FULL + buf), (g / L::NBUF) & 1, ctl)))) break;
+        if (issuer) {
           tc_fence_after();
           const uint32_t od = tmem + L::o_col(g & 1);
           const uint32_t pd = sdesc_lo(sbase + L::P_OFF + g % L::NPB * L::P_BYTES, 16);
-          if constexpr (KV8) {
-            const uint32_t vd = sdesc_lo(sbase + L::V_OFF + stage * L::KV_BYTES, 16);
+          const uint32_t vd = sdesc_lo(sbase + V_PLACE + stage * L::VM_BYTES, L::VM_COL);
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk)  // 32 keys each
-              umma_ss_f8_h(od, vd + (kk * 32 * L::ROW_BYTES >> 4), L::HI, pd + (kk * 32 >> 4), L::HI128, IDESC,
-                           (j > 1 || kk > 0) ? 1u : 0u);
-          } else {
-            const uint32_t vd = sdesc_lo(sbase + L::V_OFF + stage * L::KV_BYTES, L::BOX_BYTES);
-#pragma unroll
-            for (int kk = 0; kk < 8; ++kk)  // 16 keys each
-              umma_ss_h(od, vd + (kk * 2048 >> 4), L::HI, pd + ((kk >> 2) * NQ * 128 + (kk & 3) * 32 >> 4), L::HI128, IDESC,
-                        (j > 1 || kk > 0) ? 1u : 0u);
-          }
+          for (int kk = 0; kk < 8; ++kk)  // 16 keys each
+            umma_ss_h(od, vd + (kk * 2048 >> 4), L::HI128, pd + ((kk >> 2) * NQ * 128 + (kk & 3) * 32 >> 4), L::HI128, IDESC,
+                      (j > 1 || kk > 0) ? 1u : 0u);
           umma_commit(bar(L::B_PV_DONE + buf));
-          umma_commit(bar(L::B_V_EMPTY + stage));
+          if (!KV8) umma_commit(bar(L::B_V_EMPTY + stage));  // (e4m3: the converters wait for PV_DONE)
           if (j == n - 1) umma_commit(bar(L::B_O_FINAL));
         }
-        __syncwarp();
+        if (!KV8) __syncwarp();
       }
     }
-    if (lane == 0) {
+    if (issuer) {
       umma_commit(bar(L::B_DRAIN + 1));
       mbar_wait_drain(bar(L::B_DRAIN + 1), 0, 1000000000ull);
     }
@@ -385,7 +405,7 @@ __global__ void __launch_bounds__(FewLayout<D, KV8, NQ>::THREADS, 1)
     bool ok = true;
     for (int u = 0; ok; ++u) {
       const PagedItem it = paged_walk_next(p, walk, cta);
-      if (u >= L::NI && !__all_sync(0xffffffffu, mbar_wait(item_done(u), ((u / L::NI) - 1) & 1, ctl))) break;
+      if (u >= L::NI && !__all_sync(0xffffffffu, paged_wait(item_done(u), ((u / L::NI) - 1) & 1, ctl))) break;
       if (lane == 0) {
         volatile int* dst = reinterpret_cast<volatile int*>(sptr + L::ITEM_OFF + (u % L::NI) * sizeof(PagedItem));
         const int* from = reinterpret_cast<const int*>(&it);
@@ -398,7 +418,7 @@ __global__ void __launch_bounds__(FewLayout<D, KV8, NQ>::THREADS, 1)
       int j = one_loader ? it.n_loads : 0;
       auto load_v = [&] {
         const int s = vn % L::ST;
-        if (vn >= L::ST && !(ok = __all_sync(0xffffffffu, mbar_wait(bar(L::B_V_EMPTY + s), ((vn / L::ST) - 1) & 1, ctl))))
+        if (vn >= L::ST && !(ok = __all_sync(0xffffffffu, paged_wait(bar(L::B_V_EMPTY + s), ((vn / L::ST) - 1) & 1, ctl))))
           return;
         load_block<L::NBOX, L::ROW_BYTES>(p, &tm_v, sbase + L::V_OFF + s * L::KV_BYTES, bar(L::B_V_FULL + s), win, it.seq,
                                           it.head, it.len, it.j0 + j, lane);
@@ -408,7 +428,7 @@ __global__ void __launch_bounds__(FewLayout<D, KV8, NQ>::THREADS, 1)
         if (it.n_loads > 0) {
           for (; j < it.n_loads && vn < L::ST; ++j) load_v();  // (the first blocks, while the ring is empty)
           const int qs = qn % L::NQB;
-          if (qn >= L::NQB && !__all_sync(0xffffffffu, mbar_wait(bar(L::B_Q_EMPTY + qs), (qn / L::NQB - 1) & 1, ctl))) break;
+          if (qn >= L::NQB && !__all_sync(0xffffffffu, paged_wait(bar(L::B_Q_EMPTY + qs), (qn / L::NQB - 1) & 1, ctl))) break;
           ++qn;
           // 16 dims of a row per lane, D / 16 lanes side by side on a row; a loop, not unrolled: this runs once or
           // twice per CTA, and fetching its instructions is what it costs (unrolled over a whole row: 10k clk)
@@ -462,8 +482,33 @@ __global__ void __launch_bounds__(FewLayout<D, KV8, NQ>::THREADS, 1)
       const int n = vn - 1 - i;
       mbar_wait_drain(bar(L::B_V_FULL + n % L::ST), (n / L::ST) & 1, 1000000000ull);
     }
+  } else if (KV8 && warp >= 12) {
+    // ===================== converters: V from e4m3 to fp16 =====================
+    const int tid = threadIdx.x - 384;
+    int n = 0;
+    bool ok = true;
+    for (int u = 0; ok; ++u) {
+      if (!(ok = __all_sync(0xffffffffu, wait_item(u)))) break;
+      const volatile PagedItem* it = item_at(u);
+      const int row0 = it->row0, len = it->len, j0 = it->j0, n_loads = it->n_loads;
+      mbar_arrive_warp(item_done(u));
+      if (row0 < 0) break;
+      for (int j = 0; j < n_loads; ++j, ++n) {
+        const int s = n % L::ST, sm = KV8 ? n % max(L::VMST, 1) : 0;
+        ok = paged_wait(bar(L::B_V_FULL + s), (n / L::ST) & 1, ctl);
+        // P V has read the block converted into the same place
+        const int before = n - L::VMST;
+        if (ok && before >= 0) ok = paged_wait(bar(L::B_PV_DONE + before % L::NBUF), (before / L::NBUF) & 1, ctl);
+        if (!(ok = __all_sync(0xffffffffu, ok))) break;
+        const int live = len - (j0 + j) * L::BN;  // rows past the sequence's end become zeros
+        convert_block<D>(sptr + L::V_OFF + s * L::KV_BYTES, sptr + L::VM_OFF + sm * L::VM_BYTES, live, tid);
+        mbar_arrive_warp(bar(L::B_VM_FULL + sm));
+        mbar_arrive_warp(bar(L::B_V_EMPTY + s));
+      }
+    }
   } else {
     // ===================== softmax warpgroups =====================
+    if constexpr (KV8) setmaxnreg_inc<L::REG_SOFTMAX>();
     const int t = warp >> 2, wq = warp & 3;
     const int key = threadIdx.x & 127;  // of the block; == TMEM lane
     const uint32_t lane_addr = static_cast<uint32_t>(wq * 32) << 16;
@@ -472,15 +517,15 @@ __global__ void __launch_bounds__(FewLayout<D, KV8, NQ>::THREADS, 1)
     float* const moved = reinterpret_cast<float*>(sptr + L::MOVED_OFF) + t * 2 * NQ;
     float* const fac = reinterpret_cast<float*>(sptr + L::FAC_OFF);
     const int* const pos_of = reinterpret_cast<const int*>(sptr + L::POS_OFF);
-    // where this thread's key sits in a P row: bf16 64-key columns, e4m3 one 128-key column
-    const uint32_t p_chunk = KV8 ? key >> 4 : (key & 63) >> 3;
-    const uint32_t p_at = KV8 ? (key & 15) : (key >> 6) * (NQ * 128) + (key & 7) * 2;
+    // where this thread's key sits in a P row: 64-key columns of 16-bit values
+    const uint32_t p_chunk = (key & 63) >> 3;
+    const uint32_t p_at = (key >> 6) * (NQ * 128) + (key & 7) * 2;
     int g = 0;             // blocks of the CTA before this piece
     int items = 0;         // pieces with blocks
     // A wait that gave up (ok = false) must not leave the warpgroup's other warps at a barrier: the warp goes on to
     // the next vote (at a piece's start, or in a block), where all of them leave together.
     bool ok = true, failed = false;
-    auto wait_for = [&](int slot, int phase) { ok = ok && __all_sync(0xffffffffu, mbar_wait(bar(slot), phase & 1, ctl)); };
+    auto wait_for = [&](int slot, int phase) { ok = ok && __all_sync(0xffffffffu, paged_wait(bar(slot), phase & 1, ctl)); };
     for (int u = 0; !failed; ++u) {
       wait_for(L::B_ITEM_FULL + u % L::NI, u / L::NI);
       if (group_any(1 + t, !ok)) break;
@@ -574,7 +619,7 @@ __global__ void __launch_bounds__(FewLayout<D, KV8, NQ>::THREADS, 1)
             // the stream's earlier P V must be complete before its accumulator is scaled
             wait_for(L::B_PV_DONE + (gg - 2) % L::NBUF, (gg - 2) / L::NBUF);
             tc_fence_after();
-            tmem_scale_cols<L::NS>(tmem + lane_addr + L::o_col(t), moved + NQ, NQ);
+            tmem_scale_cols<NQ>(tmem + lane_addr + L::o_col(t), moved + NQ);
           }
         }
         if (L::NPB == 2 && gg >= 2) wait_for(L::B_PV_DONE + (gg - 2) % L::NBUF, (gg - 2) / L::NBUF);  // its P is read
@@ -586,18 +631,9 @@ __global__ void __launch_bounds__(FewLayout<D, KV8, NQ>::THREADS, 1)
           l[q + 1] += e1;
           uint8_t* const a0 = pb + q * 128 + ((p_chunk ^ (q & 7)) << 4);
           uint8_t* const a1 = pb + (q + 1) * 128 + ((p_chunk ^ ((q + 1) & 7)) << 4);
-          if constexpr (KV8) {
-            uint32_t hi, lo;
-            split16_e4m3x2(e0, e1, hi, lo);
-            a0[0] = static_cast<uint8_t>(hi);
-            a1[0] = static_cast<uint8_t>(hi >> 8);
-            a0[NQ * 128] = static_cast<uint8_t>(lo);
-            a1[NQ * 128] = static_cast<uint8_t>(lo >> 8);
-          } else {
-            const uint32_t w = pack_bf16x2(e0, e1);
-            *reinterpret_cast<uint16_t*>(a0) = static_cast<uint16_t>(w);
-            *reinterpret_cast<uint16_t*>(a1) = static_cast<uint16_t>(w >> 16);
-          }
+          const uint32_t w = KV8 ? pack_f16x2(e0, e1) : pack_bf16x2(e0, e1);
+          *reinterpret_cast<uint16_t*>(a0) = static_cast<uint16_t>(w);
+          *reinterpret_cast<uint16_t*>(a1) = static_cast<uint16_t>(w >> 16);
         }
         // the first P of a piece lets P V overwrite this stream's accumulator: stream 0 has read it (at the last piece's end)
         if (first && t == 1 && items > 0) wait_for(L::B_XCHG_READ, items - 1);
@@ -675,18 +711,12 @@ __global__ void __launch_bounds__(FewLayout<D, KV8, NQ>::THREADS, 1)
 #pragma unroll
           for (int st = 0; st < 2; ++st) {
             if (!(st == 0 ? have_a : have_b)) continue;
-            uint32_t hi[16];
-            tmem_ld_cols<16>(tmem + lane_addr + L::o_col(st) + c0, hi);
-            if constexpr (KV8) {
-              uint32_t lo[16];
-              tmem_ld_cols<16>(tmem + lane_addr + L::o_col(st) + NQ + c0, lo);
-#pragma unroll
-              for (int q = 0; q < 16; ++q) hi[q] = __float_as_uint(fmaf(__uint_as_float(lo[q]), L::LO, __uint_as_float(hi[q])));
-            }
+            uint32_t acc[16];
+            tmem_ld_cols<16>(tmem + lane_addr + L::o_col(st) + c0, acc);
 #pragma unroll
             for (int q = 0; q < 16; ++q) {
               const float w = fac[st * NQ + c0 + q];
-              if (w > 0.f) x[q] = fmaf(__uint_as_float(hi[q]), w, x[q]);
+              if (w > 0.f) x[q] = fmaf(__uint_as_float(acc[q]), w, x[q]);
             }
           }
           if (d < 0) continue;

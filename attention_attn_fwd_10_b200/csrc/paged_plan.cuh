@@ -124,6 +124,7 @@ __device__ __forceinline__ long long head_steps(const PagedParams& p, const SeqW
     o.diag = __shfl_sync(0xffffffffu, w.diag, src);
     o.units = __shfl_sync(0xffffffffu, w.units, src);
     long long part = 0;
+#pragma unroll 1
     for (int u = lane; u < o.units; u += 32) part += unit_steps(p, o, u, as);
     part = warp_sum(part);
     if (lane == src) mine = part;

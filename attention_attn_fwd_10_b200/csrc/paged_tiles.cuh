@@ -1,10 +1,42 @@
-// Loading a paged cache's 128-key blocks, and e4m3 pairs: shared by the paged attention kernels.
+// Loading a paged cache's 128-key blocks, turning e4m3 values into fp16, and e4m3 pairs: shared by the paged
+// attention kernels.
 #pragma once
 
 #include "paged_plan.cuh"
 #include "sm100_common.cuh"
 
 namespace attn {
+
+// True in one lane of a converged warp.  A branch on it, unlike one on the lane's number, keeps what it issues in
+// uniform registers: the MMAs of a block leave sooner.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r));
+  return r != 0;
+}
+
+// mbar_wait in fewer instructions: where many warps of different roles wait inside loops, the copies of its code
+// fill the instruction cache.
+__device__ __forceinline__ bool paged_wait(uint32_t bar, uint32_t parity, const WaitCtl& ctl) {
+  uint64_t t0 = 0;
+#pragma unroll 1
+  for (uint32_t it = 0; !mbar_try_wait(bar, parity); ++it) {
+    if ((it & 15u) != 0) continue;
+    if (*ctl.abort_flag) return false;
+    const uint64_t now = globaltimer_ns();
+    if (it == 0) t0 = now;
+    if (now - t0 > ctl.limit_ns) {
+      *ctl.abort_flag = 1;
+      atomicExch(ctl.status, kDevWaitTimeout);
+      return false;
+    }
+  }
+  return true;
+}
 
 // x as a sum of two e4m3 values, pairs of them in the low 16 bits (the first value in the low byte):
 //   hi = e4m3(x), lo = e4m3((x - hi) * factor).
@@ -96,6 +128,59 @@ __device__ __forceinline__ void zero_tail(uint8_t* tile, int live, int lane) {
       *reinterpret_cast<uint4*>(tile + x * 128 * ROW_BYTES + c * 16) = zero;
   fence_proxy_async_smem();
   __syncwarp();
+}
+
+// Turns a landed e4m3 block of V into fp16 (exactly), by 128 threads: src as loaded, one column of D-byte rows;
+// dst D / 64 columns of 128-byte rows, swizzled as the MMAs read them.  Rows past the sequence's end (`live` keys are
+// its own) become zeros.  Visible to the tensor cores.
+//
+// A thread takes 16 dims of a key at a time: a 16-byte chunk in, two out.  Eight lanes that access shared memory
+// together have four chunks of two keys.  D = 128: keys k and k ^ 5, whose swizzles set the chunks apart both as read
+// (bit 2 of the key) and as written (bit 0); one key's eight chunks would meet in the banks as they are written, four to
+// each of the two columns.  A thread's keys are 32 apart, so that all its swizzles are the same and every address is a
+// constant off four bases: the warps of this loop share the instruction cache with four other roles.
+template <int D>
+__device__ __forceinline__ void convert_block(const uint8_t* src, uint8_t* dst, int live, int tid) {
+  const int key0 = D == 128 ? tid / 32 * 8 + ((tid >> 3 & 3) ^ ((tid >> 2 & 1) * 5)) : tid / 4, c = tid & 3;
+  const int sw = D == 128 ? (key0 & 7) : ((key0 >> 1) & 3);
+  const uint8_t* const in = src + key0 * D + ((c ^ sw) * 16);
+  const uint8_t* const in4 = src + key0 * D + (((c + 4) ^ sw) * 16);  // D = 128: chunk c + 4
+  uint8_t* const out0 = dst + key0 * 128 + (((2 * c) ^ (key0 & 7)) * 16);
+  uint8_t* const out1 = dst + key0 * 128 + (((2 * c + 1) ^ (key0 & 7)) * 16);
+#pragma unroll 1
+  for (int i = 0; i < 4; ++i) {
+#pragma unroll
+    for (int col = 0; col < D / 64; ++col) {
+      const uint4 x = *reinterpret_cast<const uint4*>((col == 0 ? in : in4) + i * 32 * D);
+      const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+      uint32_t y[8];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(y[2 * k]) : "h"(static_cast<uint16_t>(w[k])));
+        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(y[2 * k + 1]) : "h"(static_cast<uint16_t>(w[k] >> 16)));
+      }
+      const int at = col * (128 * 128) + i * 32 * 128;
+      *reinterpret_cast<uint4*>(out0 + at) = make_uint4(y[0], y[1], y[2], y[3]);
+      *reinterpret_cast<uint4*>(out1 + at) = make_uint4(y[4], y[5], y[6], y[7]);
+    }
+  }
+  if (live < 128) {  // the thread's own rows past the end
+#pragma unroll 1
+    for (int i = 0; i < 4 * (D / 64); ++i) {
+      const int at = i / 4 * (128 * 128) + (i & 3) * 32 * 128;
+      if (key0 + (i & 3) * 32 < live) continue;
+      *reinterpret_cast<uint4*>(out0 + at) = make_uint4(0, 0, 0, 0);
+      *reinterpret_cast<uint4*>(out1 + at) = make_uint4(0, 0, 0, 0);
+    }
+  }
+  fence_proxy_async_smem();
+}
+
+// Two weights as a pair of fp16.
+__device__ __forceinline__ uint32_t pack_f16x2(float x0, float x1) {
+  uint32_t w;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(x1), "f"(x0));
+  return w;
 }
 
 }  // namespace attn
