@@ -98,7 +98,10 @@ struct ChunkLayout {
   static constexpr int WARP_K = 8, WARP_MMA = 9, WARP_V = 10, WARP_SCHED = 11;
   // 2 x 128 x 216 + 128 x 72 = 384 x 168; e4m3: 2 x 128 x 200 + 256 x 56 = 512 x 128
   static constexpr int REG_LAUNCH = KV8 ? 128 : 168, REG_SOFTMAX = KV8 ? 200 : 216, REG_OTHER = KV8 ? 56 : 72;
-  static constexpr float TAU = 8.f;  // weights stay below 2^TAU
+  // Weights up to 2^(SHIFT + TAU), a row's largest at 2^SHIFT or more (paged_few_kernel.cuh says why: fp16's least
+  // steps are then 2^-31 of the largest)
+  static constexpr float SHIFT = KV8 ? 7.f : 0.f, DOWN = KV8 ? 1.f / 128.f : 1.f;  // 2^-SHIFT
+  static constexpr float TAU = 8.f;
   // shared-memory descriptors' high half: K-major Q and K, and V (MN-major)
   static constexpr uint32_t HI = ROW_BYTES == 128 ? sdesc_sw128_hi(1024) : sdesc_sw64_hi(512);
   static constexpr uint32_t HI_V = sdesc_sw128_hi(1024);
@@ -570,7 +573,7 @@ __global__ void __launch_bounds__(ChunkLayout<D, KV8>::THREADS, 1)
             if (cc > lim_c) s[cc] = -INFINITY;
         }
         const float mx = row_max128(sr);
-        const float m_new = fmaxf(m_used, mx * c);
+        const float m_new = fmaxf(m_used, mx * c - L::SHIFT);
         const bool resc = (m_new - m_used) > L::TAU;  // false for NaN (-inf - -inf)
         float alpha = 1.f;
         if (resc) {
@@ -633,7 +636,8 @@ __global__ void __launch_bounds__(ChunkLayout<D, KV8>::THREADS, 1)
           const float lsum = l * w_a + l_b * w_b;
           const float inv_l = lsum > 0.f ? p.v_scale / lsum : 0.f;
           const float c_a = w_a * inv_l, c_b = w_b * inv_l;
-          const float lse2 = lsum > 0.f ? mx + __log2f(lsum) : -INFINITY;
+          // (the power of two taken out first: the logarithm's error grows with its size)
+          const float lse2 = lsum > 0.f ? mx + L::SHIFT + __log2f(lsum * L::DOWN) : -INFINITY;
           const uint32_t oa_addr = tmem + lane_addr + L::o_col(t);
           const uint32_t ob_addr = tmem + lane_addr + L::o_col(1);
           const int slot = it->slot;

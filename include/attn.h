@@ -303,8 +303,8 @@ attn_status_t attn_paged_append(const attn_paged_kv_t* cache, const void* q, con
  * they hold; q and the keys and values before it must be finite.  An e4m3 cache costs
  * no accuracy beyond its own rounding: its K and V are used as they are, q as the sum of two e4m3
  * terms (exact down to 2^-17 of a row's largest element), and the softmax weights as fp16, where a bf16
- * cache has them as bf16.  A small fp16 weight may be off by 2^-25 of the row's largest, 2^-32 where the rows of a kv
- * group are few.  The same call on the same lengths gives the same bits.
+ * cache has them as bf16; a small fp16 weight may be off by 2^-32 of the row's largest.
+ * The same call on the same lengths gives the same bits.
  *   q        : bf16, token stride q_stride elements (a multiple of 8, >= H_q * D).
  *   H_q      : a multiple of the cache's H_kv, H_q / H_kv <= 128.
  *   max_new  : the most new tokens of any sequence, as far as the caller knows: it

@@ -97,3 +97,9 @@ def test_one_key_far_above(n_seq, keys, D, gap, e4m3, hint):
 @pytest.mark.parametrize("hint", [4, 8, 400])  # 16 and 32 columns of real rows, tiles
 def test_one_key_far_above_grouped_drafts(hint):
     _check(40, 20000, 8, 2, 128, 12.0, True, hint, new=4)
+
+
+@pytest.mark.parametrize("hint", [1, 20, 400])
+def test_one_key_far_above_a_million(hint):
+    # 18.5 nats: each other weight is near 2^-27 of the largest, all together 1 % of the row
+    _check(148, 1 << 20, 1, 1, 64, 18.5, True, hint)
