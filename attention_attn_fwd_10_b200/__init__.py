@@ -290,7 +290,9 @@ class FwdBwdPipeline:
     with the copies of one step overlapping the kernels of its neighbours.
 
     ``rotary`` (with ``positions`` on the device as in ``rope``): q and k are rotated before
-    the forward, and dq, dk are the gradients of the unrotated q and k.
+    the forward, and dq, dk are the gradients of the unrotated q and k.  A step's rotations run
+    after what the current stream holds when the step is submitted, so both may have been written
+    there; before they are changed in place, ``synchronize()``.
 
     Three streams: the inputs of a step (q, k, v, dO) go up on one copy stream,
     its kernels run on a compute stream, and its results (o, lse, dq, dk, dv)
@@ -349,6 +351,8 @@ class FwdBwdPipeline:
             s["uploaded"].record(self.up)
         self.compute.wait_event(s["uploaded"])
         if self.rotary is not None:
+            # inv_freq and positions are the caller's device tensors
+            self.compute.wait_stream(torch.cuda.current_stream(self.dev))
             rope(s["q"], s["k"], rotary=self.rotary, positions=self.positions, q_out=s["q"], k_out=s["k"],
                  stream=self.compute)
         fwd(s["q"], s["k"], s["v"], causal=self.causal, scale=self.scale, out=s["o"], lse=s["lse"],
