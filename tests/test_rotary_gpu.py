@@ -207,3 +207,52 @@ def test_training_step_needs_equal_lengths():
         attn.fwd_bwd(q, k, k, q, rotary=r)
     with pytest.raises(ValueError, match="S_q == S_k"):
         attn.FwdBwdPipeline(1, 4, 5, 1, 1, 64, rotary=r)
+
+
+@pytest.mark.parametrize("H_q,H_kv", [(2, 2), (4, 1)])
+@pytest.mark.parametrize("pipeline", [False, True])
+def test_training_step_gradients_along_themselves(pipeline, H_q, H_kv):
+    """dq and dk against the formula's as a whole, and against the fp64 loss's slope along the formula's: that
+    direction's slope is the gradient's squared norm, so a gradient that is missing, negated or left unrotated shows.
+
+    Tolerance, relative to the gradient's norm: rounding to bf16 is at most 2^-8 of a value, 2^-8 / sqrt(3) rms.  q' and
+    k': a score (rms 1) is off by sqrt(2) times that; P's rounding, dS's, k' (q') in the product, and the gradient's two
+    (before and after it is turned back): sqrt(2 + 1 + 1 + 1 + 2) 2^-8 / sqrt(3) = 6e-3 in all; 2^-6 holds it 2.6 times."""
+    attn = _attn()
+    B, S, D = 2, 130, 64
+    g = torch.Generator().manual_seed(13)
+    q, do = (torch.randn((B, S, H_q, D), generator=g).bfloat16() for _ in range(2))
+    k, v = (torch.randn((B, S, H_kv, D), generator=g).bfloat16() for _ in range(2))
+    where = torch.randint(0, 5000, (B, S), generator=g, dtype=torch.int32)
+    freq, scale = _freq(32), D ** -0.5
+    rotary = attn.Rotary(freq.cuda())
+    if pipeline:
+        out = {n: torch.empty_like(t).pin_memory() for n, t in (("o", q), ("dq", q), ("dk", k), ("dv", v))}
+        out["lse"] = torch.empty((B, H_q, S)).pin_memory()
+        pipe = attn.FwdBwdPipeline(B, S, S, H_q, H_kv, D, causal=True, rotary=rotary, positions=where.cuda())
+        pipe.submit(*(t.pin_memory() for t in (q, k, v, do)), out)
+        pipe.synchronize()
+    else:
+        out = attn.fwd_bwd(q, k, v, do, causal=True, rotary=rotary, positions=where)
+    assert attn.device_status() == 0
+    pos = where.reshape(1, -1).numpy()
+    q64, k64, v64, do64 = (ref.to_f64(t) for t in (q, k, v, do))
+
+    def turn(x, inverse=False):
+        return oracle.rotate(x.reshape(B * S, *x.shape[2:]), pos, freq, inverse=inverse).reshape(x.shape)
+
+    dqr, dkr, dv = ref.backward(turn(q64), turn(k64), v64, do64, True, scale)
+    want = {"dq": turn(dqr, inverse=True), "dk": turn(dkr, inverse=True), "dv": dv}
+    for name, w in want.items():
+        got = parity.to_np(out[name])
+        assert np.linalg.norm(got - w) <= 2.0 ** -6 * np.linalg.norm(w), name
+    for name in ("dq", "dk"):
+        w, h = want[name], 1e-5
+        loss = []
+        for sgn in (1, -1):
+            at = {"dq": q64, "dk": k64}
+            at[name] = at[name] + sgn * h * w
+            loss.append(_loss(at["dq"], at["dk"], v64, do64, pos, freq, scale)[0])
+        slope = (loss[0] - loss[1]) / (2 * h)
+        assert abs(float((w * w).sum()) - slope) <= 1e-5 * slope, name  # the formula itself
+        assert abs(float((parity.to_np(out[name]) * w).sum()) - slope) <= 2.0 ** -6 * slope, name
