@@ -182,6 +182,17 @@ __global__ void __launch_bounds__(kRotThreads, 4) rotary_kernel(const RotaryPara
   }
 
   if (PAGED) {
+    // Ranges and lengths, owned by a token or not (the look-up below meets only those that are), by the grid's
+    // threads from each CTA's last warp on: the first ones have tokens to look up.
+    if (blockIdx.y == 0) {
+      for (long long b = static_cast<long long>(blockIdx.x) * kRotThreads + (kRotThreads - 1 - tid); b < p.n_seq;
+           b += static_cast<long long>(gridDim.x) * kRotThreads) {
+        const int start = p.q_start[b], end = p.q_start[b + 1], len = p.seq_len[b];
+        if (start < 0 || end < start || end > p.n_tokens || len < 0 ||
+            len > static_cast<long long>(p.max_pages) * p.page_size)
+          atomicExch(p.status, kDevBadIndex);
+      }
+    }
     if (warp < nt) {
       const long long t = t0 + warp;
       const int b = owner_of(t, p.q_start, p.n_seq, lane);

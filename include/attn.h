@@ -263,9 +263,9 @@ attn_status_t attn_rope(const void* q, const void* k, void* q_out, void* k_out, 
  * The three index arrays are read on the device when the call runs (a captured call
  * reads their contents at replay).  Entries that lead outside the cache -- a page not in
  * [0, n_pages) among those a sequence needs, a length beyond max_pages * page_size,
- * more new tokens than keys in an append, a token range outside [0, n_tokens] -- never cause an access
- * out of range: the call records ATTN_ERR_BAD_INDEX in the device status word and the
- * results of that sequence are undefined.
+ * more new tokens than keys in an append, a token range outside [0, n_tokens] or running backwards -- never cause an
+ * access out of range: the call records ATTN_ERR_BAD_INDEX in the device status word and the
+ * results of that sequence (of a range that runs backwards: of the sequences before and behind it too) are undefined.
  */
 typedef struct {
   void* k;

@@ -534,6 +534,46 @@ def test_bad_indices_are_reported(what, hint):
     assert torch.equal(o, good[0]) and attn.device_status() == 0
 
 
+@pytest.mark.parametrize("starts", [[0, 4, 1000000], [0, 5, 3], [0, 4, 3, 4], [0, 4, -2], [0, 4, 4, 5], [0] * 300 + [4, 9]])
+@pytest.mark.parametrize("op", ["append", "attend"])
+def test_bad_ranges_without_rows_are_reported(op, starts):
+    """Ranges that no token row belongs to: past the rows, running backwards, among many sequences."""
+    attn = _attn()
+    n = len(starts) - 1
+    T, page = 4, 16
+    kc, vc = (torch.zeros((8, page, 1, 64), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    table = (torch.arange(n * 2, dtype=torch.int32, device="cuda") % 8).view(n, 2)
+    lens = torch.full((n,), 20, dtype=torch.int32, device="cuda")
+
+    def call(s):
+        start = torch.tensor(s, dtype=torch.int32, device="cuda")
+        x = torch.ones((T, 1, 64), dtype=torch.bfloat16, device="cuda")
+        cache = attn.PagedKV(kc, vc, table, lens, start)
+        if op == "append":
+            attn.paged_append(cache, x, x)
+        else:
+            attn.fwd_paged(cache, x, max_new=1)
+        return attn.device_status()
+
+    assert call(starts) == 7
+    assert call([0] + [T] * n) == 0
+
+
+@pytest.mark.parametrize("length", [-1, 33, 2 ** 31 - 1])
+def test_bad_lengths_without_rows_are_reported(length):
+    attn = _attn()
+    kc, vc = (torch.zeros((8, 16, 1, 64), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    table = torch.arange(4, dtype=torch.int32, device="cuda").view(2, 2)
+    start = torch.tensor([0, 4, 4], dtype=torch.int32, device="cuda")
+    x = torch.ones((4, 1, 64), dtype=torch.bfloat16, device="cuda")
+    for n, want in ((length, 7), (32, 0), (0, 0)):
+        cache = attn.PagedKV(kc, vc, table, torch.tensor([20, n], dtype=torch.int32, device="cuda"), start)
+        attn.paged_append(cache, x, x)
+        assert attn.device_status() == want
+        attn.fwd_paged(cache, x)
+        assert attn.device_status() == want
+
+
 def test_refusals():
     attn = _attn()
     d = to_gpu(make([1], [40], 4, 2, 64, 16, seed=17))
