@@ -65,13 +65,23 @@ def _rows(name, t, dev, H=None, D=None):
     return tokens, h, d, step if tokens > 1 else h * d
 
 
-class Rotary:
+class _Fixed:
+    """Attributes are set once: the calls go by what the constructor checked."""
+
+    def __setattr__(self, name, value):
+        # (`cache.seq_len += 1` assigns the tensor it changed in place)
+        if name in self.__dict__ and value is not self.__dict__[name]:
+            raise AttributeError(f"{name} cannot be replaced: write into it, or make a new {type(self).__name__}")
+        super().__setattr__(name, value)
+
+
+class Rotary(_Fixed):
     """The frequencies of a rotation (attn_rotary_t).
 
     ``inv_freq``: fp32 CUDA tensor [n_freq]; the first 2 n_freq dims of a head turn.
     ``sections``: frequencies of each position axis, in order (default: one axis).
     ``interleaved``: pairs are dims (2i, 2i + 1) instead of (i, i + n_freq).
-    The tensor is kept; its contents are read by each call."""
+    The tensor is kept; its contents are read by each call.  Attributes cannot be replaced."""
 
     def __init__(self, inv_freq: torch.Tensor, sections=None, interleaved: bool = False):
         if inv_freq.dtype != torch.float32 or inv_freq.dim() != 1 or not inv_freq.is_contiguous():
@@ -149,7 +159,7 @@ def rope(q, k=None, *, rotary: Rotary, positions=None, inverse: bool = False, q_
     return q_out if k is None else (q_out, k_out)
 
 
-class PagedKV:
+class PagedKV(_Fixed):
     """A paged key/value cache and the batch of sequences a call works on (attn_paged_kv_t).
 
     ``k``, ``v``: [n_pages, page_size, H_kv, D] bf16 or torch.float8_e4m3fn CUDA tensors of the
@@ -160,7 +170,7 @@ class PagedKV:
     ``k_scale``, ``v_scale``: an e4m3 cache holds k / k_scale and v / v_scale.
 
     The tensors are kept and their contents read on the device by each call, so a step updates them in
-    place (inside a CUDA graph too); they may not be resized."""
+    place (inside a CUDA graph too); they may not be resized, and the attributes cannot be replaced."""
 
     def __init__(self, k, v, page_table, seq_len, q_start, k_scale: float = 1.0, v_scale: float = 1.0):
         if k.dim() != 4 or k.shape != v.shape or k.stride() != v.stride():

@@ -559,6 +559,28 @@ def test_bad_ranges_without_rows_are_reported(op, starts):
     assert call([0] + [T] * n) == 0
 
 
+def test_handles_follow_their_tensors_or_refuse():
+    """The handle goes by what it was made of: changed in place it follows, a replacement is refused."""
+    attn = _attn()
+    x = make([1, 1], [100, 60], 4, 2, 128, 16, seed=18)
+    g = to_gpu(x)
+    cache = handle(attn, g)
+    cache.seq_len -= 1  # in place
+    o, _ = attn.fwd_paged(cache, g["q"])
+    y = make([1, 1], [100, 60], 4, 2, 128, 16, seed=18)
+    y["seq_len"] = y["seq_len"] - 1
+    h = to_gpu(y)
+    assert torch.equal(o, attn.fwd_paged(handle(attn, h), h["q"])[0])
+    for name, value in (("seq_len", g["seq_len"] + 1), ("page_table", g["page_table"].clone()), ("k", g["k_cache"].clone()),
+                        ("q_start", g["q_start"].clone()), ("v", g["v_cache"].clone()), ("k_scale", 2.0), ("H_kv", 1)):
+        with pytest.raises(AttributeError, match=name):
+            setattr(cache, name, value)
+    r = attn.Rotary(_freq(64).cuda())
+    for name, value in (("inv_freq", _freq(32).cuda()), ("sections", (32, 32)), ("interleaved", True)):
+        with pytest.raises(AttributeError, match=name):
+            setattr(r, name, value)
+
+
 @pytest.mark.parametrize("length", [-1, 33, 2 ** 31 - 1])
 def test_bad_lengths_without_rows_are_reported(length):
     attn = _attn()
