@@ -350,6 +350,9 @@ attn_status_t attn_fwd_paged(const attn_paged_kv_t* c, const void* q, void* o, f
   if (!q || !o || !lse || !workspace || H_q < 1 || H_q % c->H_kv != 0 || !good_stride(q_stride, H_q, c->D))
     return ATTN_ERR_INVALID_ARG;
   if (max_new < 0 || (causal != 0 && causal != 1) || !std::isfinite(scale) || !(scale > 0.f)) return ATTN_ERR_INVALID_ARG;
+  // what turns a product of q and a stored key into a score in base-2 units
+  const double scale_log2 = static_cast<double>(scale) * c->k_scale * 1.4426950408889634;
+  if (scale_log2 > 3.4028234e38) return ATTN_ERR_INVALID_ARG;
   if (H_q / c->H_kv > 128) return ATTN_ERR_UNSUPPORTED;
   if (!aligned(q, 16) || !aligned(o, 16) || !aligned(lse, 16) || !aligned(workspace, 32)) return ATTN_ERR_MISALIGNED;
   if (n_tokens == 0) return ATTN_OK;
@@ -374,7 +377,7 @@ attn_status_t attn_fwd_paged(const attn_paged_kv_t* c, const void* q, void* o, f
   p.page_table = c->page_table;
   p.seq_len = c->seq_len;
   p.q_start = c->q_start;
-  p.scale_log2 = std::max(static_cast<float>(static_cast<double>(scale) * c->k_scale * 1.4426950408889634), 1.17549435e-38f);
+  p.scale_log2 = std::max(static_cast<float>(scale_log2), 1.17549435e-38f);
   p.v_scale = c->v_scale;
   p.causal = causal;
   p.wait_limit_ns = api_wait_limit_ns();

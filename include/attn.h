@@ -307,6 +307,7 @@ attn_status_t attn_paged_append(const attn_paged_kv_t* cache, const void* q, con
  * The same call on the same lengths gives the same bits.
  *   q        : bf16, token stride q_stride elements (a multiple of 8, >= H_q * D).
  *   H_q      : a multiple of the cache's H_kv, H_q / H_kv <= 128.
+ *   scale    : > 0; scale * k_scale * log2(e) must be finite in 32 bits.
  *   max_new  : the most new tokens of any sequence, as far as the caller knows: it
  *              chooses the kernel, and any value gives the same result up to rounding.  0 = unknown.
  *   workspace: device, 32-byte aligned, attn_fwd_paged_workspace_size(H_q, H_kv, D)

@@ -63,6 +63,13 @@ def test_attend_refusals(lib, kw, code):
     assert lib.attn_fwd_paged(None, a["q"], a["o"], a["lse"], a["ws"], a["T"], a["H_q"], a["stride"], 0, 1, 0.125, None) == 1
 
 
+@pytest.mark.parametrize("scale,k_scale,code", [(1e30, 1e10, 1), (3e38, 1.5, 1), (2.5e38, 1.0, 1), (2.3e38, 1.0, 0), (1e-30, 1e30, 0)])
+def test_scales_whose_product_overflows_are_refused(lib, scale, k_scale, code):
+    # scale * k_scale * log2(e) is held in 32 bits: infinite, it would make NaN of a score of 0
+    c = _cache(e4m3=1, k_scale=k_scale)
+    assert lib.attn_fwd_paged(ctypes.byref(c), 16, 32, 48, 64, 0, 4, 256, 0, 1, scale, None) == code
+
+
 def _rotary(**kw):
     a = dict(inv_freq=0x6000, positions=0x7000, n_freq=32, n_axes=1, section=(ctypes.c_int * 4)(32, 0, 0, 0), interleaved=0)
     a.update(kw)
