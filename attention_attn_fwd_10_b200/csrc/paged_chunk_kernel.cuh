@@ -634,7 +634,7 @@ __global__ void __launch_bounds__(ChunkLayout<D, KV8>::THREADS, 1)
           const float w_a = l > 0.f ? exp2_mufu(m_used - mx) : 0.f;
           const float w_b = l_b > 0.f ? exp2_mufu(m_b - mx) : 0.f;
           const float lsum = l * w_a + l_b * w_b;
-          const float inv_l = lsum > 0.f ? p.v_scale / lsum : 0.f;
+          const float inv_l = lsum > 0.f ? 1.f / lsum : 0.f;
           const float c_a = w_a * inv_l, c_b = w_b * inv_l;
           // (the power of two taken out first: the logarithm's error grows with its size)
           const float lse2 = lsum > 0.f ? mx + L::SHIFT + __log2f(lsum * L::DOWN) : -INFINITY;
@@ -661,7 +661,7 @@ __global__ void __launch_bounds__(ChunkLayout<D, KV8>::THREADS, 1)
             for (int i = 0; i < 16; ++i) {
               float v = (nb > 0 && w_a > 0.f) ? __uint_as_float(orr[i]) * c_a : 0.f;
               if (have_b && w_b > 0.f) v += __uint_as_float(obr[i]) * c_b;
-              ov[i] = v;
+              ov[i] = KV8 ? v * p.v_scale : v;
             }
             if (!valid) continue;
             if (slot >= 0) {

@@ -679,7 +679,7 @@ __global__ void __launch_bounds__(FewLayout<D, KV8, NQ>::THREADS, 1)
           const float top = fmaxf(la > 0.f ? ma : kNoKeyYet, lb > 0.f ? mb : kNoKeyYet);
           const float wa = la > 0.f ? exp2_mufu(ma - top) : 0.f, wb = lb > 0.f ? exp2_mufu(mb - top) : 0.f;
           const float sum = la * wa + lb * wb;
-          const float inv = sum > 0.f ? p.v_scale / sum : 0.f;
+          const float inv = sum > 0.f ? 1.f / sum : 0.f;
           fac[q] = wa * inv;
           fac[NQ + q] = wb * inv;
           if (q < real) {
@@ -720,6 +720,10 @@ __global__ void __launch_bounds__(FewLayout<D, KV8, NQ>::THREADS, 1)
             }
           }
           if (d < 0) continue;
+          if constexpr (KV8) {  // (not in the factors: v_scale / sum may be too small for 32 bits where the product is not)
+#pragma unroll
+            for (int q = 0; q < 16; ++q) x[q] *= p.v_scale;
+          }
 #pragma unroll
           for (int q = 0; q < 16; ++q) {
             if (c0 + q >= real) break;

@@ -103,3 +103,27 @@ def test_one_key_far_above_grouped_drafts(hint):
 def test_one_key_far_above_a_million(hint):
     # 18.5 nats: each other weight is near 2^-27 of the largest, all together 1 % of the row
     _check(148, 1 << 20, 1, 1, 64, 18.5, True, hint)
+
+
+@pytest.mark.parametrize("hint", [1, 20, 400])
+@pytest.mark.parametrize("n_seq,keys", [(1, 700), (1, 20000), (300, 20000)])
+@pytest.mark.parametrize("v_scale", [2.0 ** -124, 2.0 ** 110])
+def test_value_scales_at_the_ends(hint, n_seq, keys, v_scale):
+    """A power of two as v_scale changes the output's exponent and nothing else (sums, factors and pieces in 32 bits
+    have room for it; an output above 2^-126 is a normal number)."""
+    q, cache = _batch(n_seq, keys, 2, 1, 128, 0.0, True)
+    unit = _attn().PagedKV(cache.k, cache.v, cache.page_table, cache.seq_len, cache.q_start, k_scale=cache.k_scale)
+    scaled = _attn().PagedKV(cache.k, cache.v, cache.page_table, cache.seq_len, cache.q_start, k_scale=cache.k_scale,
+                             v_scale=v_scale)
+    o1, lse1 = _attn().fwd_paged(unit, q, causal=False, max_new=hint)
+    o2, lse2 = _attn().fwd_paged(scaled, q, causal=False, max_new=hint)
+    assert _attn().device_status() == 0
+    assert torch.equal(lse1, lse2)
+    want = o1.double() * v_scale
+    normal = (want.abs() >= 2.0 ** -125) & (o1 != 0)
+    # (what is checked: at 2^-124 all but outputs below 1/2; they are near 25 N(0, 1), each channel's mean as stored: 1.6 %)
+    assert float(normal.float().mean()) > 0.95
+    # the pieces' fp32 rows lose nothing above 2^-126 either: what is left is one bf16 step where a piece's part is below it
+    off = (o2.double() - want).abs()
+    assert bool((off[normal] <= 2.0 ** -7 * want[normal].abs()).all())
+    assert float((off[normal] != 0).float().mean()) < 0.01
