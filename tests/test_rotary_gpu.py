@@ -256,3 +256,12 @@ def test_training_step_gradients_along_themselves(pipeline, H_q, H_kv):
         slope = (loss[0] - loss[1]) / (2 * h)
         assert abs(float((w * w).sum()) - slope) <= 1e-5 * slope, name  # the formula itself
         assert abs(float((parity.to_np(out[name]) * w).sum()) - slope) <= 2.0 ** -6 * slope, name
+
+
+@pytest.mark.parametrize("shape", [(64,), (4, 64), (4, 1, 64), ()])
+@pytest.mark.parametrize("rotary", [False, True])
+def test_training_step_refuses_other_shapes(shape, rotary):
+    attn = _attn()
+    x = torch.zeros(shape).bfloat16()
+    with pytest.raises(ValueError, match="4-D"):
+        attn.fwd_bwd(x, x, x, x, rotary=attn.Rotary(_freq(32).cuda()) if rotary else None)
