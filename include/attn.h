@@ -288,7 +288,7 @@ typedef struct {
  * turned into q_out (contiguous, or q itself when q_stride = H_q * D).  q NULL: only k and v; rotary NULL: no
  * rotation (then q must be NULL).  e4m3: x / scale rounded to nearest, saturated at
  * +-448, from the fp32 rotation's result (one rounding).  Two tokens that map to
- * one slot (sequences that share their last page) leave either's value there.
+ * one slot (sequences that share their last page) leave parts of either's there.
  */
 attn_status_t attn_paged_append(const attn_paged_kv_t* cache, const void* q, const void* k, const void* v, void* q_out,
                                 int n_tokens, int H_q, long long q_stride, long long k_stride, long long v_stride,
