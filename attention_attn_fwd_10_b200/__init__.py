@@ -256,7 +256,8 @@ def fwd_bwd(q, k, v, do, causal: bool = False, scale: float | None = None, host_
     current device, run the forward and the backward there, and copy o, lse,
     dq, dk, dv back into ``host_out`` (pinned CPU tensors, allocated if None).
     ``rotary``: q and k are rotated before the forward (``positions`` as in ``rope``,
-    host or device) and dq, dk are the gradients of the unrotated q and k.
+    host or device) and dq, dk are the gradients of the unrotated q and k: bwd's bf16 results turned
+    back in place, so rounded twice.
     Returns the dict of host results."""
     if rotary is not None:
         _shapes(q, k)

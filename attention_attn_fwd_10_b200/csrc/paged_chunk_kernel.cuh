@@ -29,9 +29,10 @@
 // instead of 2.1k).
 //
 // Measured (B200, the whole call on the device): 2048 new tokens at the end of 32768 keys, 32 heads over 8 of 128,
-// 1.07 TFLOP: 1000-1170 us as the power cap allows, 0.92-1.07 PFLOP/s (e4m3 cache: 1120-1150 us; the contiguous
+// 1.07 TFLOP: 1000-1170 us as the power cap allows, 0.92-1.07 PFLOP/s (e4m3 cache: 1085-1100 us; the contiguous
 // forward of the same shape: 1008 us).  Bound, as that one, by the chain softmax -> P V -> S of a tile: 3.7k clk a
 // two-tile block, 1.05k of them MMAs.
+// The weights are rounded to the 16 bits of V's MMA, bf16 (fp16 over an e4m3 cache); the row sums add the fp32 values.
 #pragma once
 
 #include <cuda_fp16.h>

@@ -260,7 +260,8 @@ def fwd_paged(cache: PagedKV, q, causal: bool = True, scale: float | None = None
     """Attention of each sequence's new tokens q [tokens, H_q, D] over its paged keys
     (attn_fwd_paged).  Returns (o bf16 [tokens, H_q, D], lse fp32 [H_q, tokens]); rows that
     belong to no sequence are left as ``out`` and ``lse`` had them.  ``max_new``: the most new
-    tokens of any sequence (chooses the kernel only; 0 = unknown)."""
+    tokens of any sequence (chooses the kernel only; 0 = unknown: the mean decides, which suits batches whose
+    sequences bring about as many each)."""
     dev = cache.device
     if q.dim() != 3:
         raise ValueError(f"q must be [tokens, H_q, D], got shape {tuple(q.shape)}")

@@ -309,7 +309,8 @@ attn_status_t attn_paged_append(const attn_paged_kv_t* cache, const void* q, con
  *   H_q      : a multiple of the cache's H_kv, H_q / H_kv <= 128.
  *   scale    : > 0; scale * k_scale * log2(e) must be finite in 32 bits.
  *   max_new  : the most new tokens of any sequence, as far as the caller knows: it
- *              chooses the kernel, and any value gives the same result up to rounding.  0 = unknown.
+ *              chooses the kernel, and any value gives the same result up to rounding.  0 = unknown: the
+ *              mean decides, and a long chunk among many single tokens may then run slowly.
  *   workspace: device, 32-byte aligned, attn_fwd_paged_workspace_size(H_q, H_kv, D)
  *              bytes; contents ignored, none kept.  Calls that may overlap need one each.
  */
