@@ -222,9 +222,9 @@ cudaError_t launch_paged(void (*kern)(CUtensorMap, CUtensorMap, CUtensorMap, Pag
 
 // The kernel by the rows that a sequence's new tokens make in a kv group (max_new, or the mean where it is not
 // known, times the group's heads): up to 32 as MMA columns, more as tiles of 128 rows.  64 sequences of up to 4096
-// keys, 8 kv heads, head dim 128, bf16 / e4m3 cache, in us: 16 rows as 16 columns 106 / 79, as 32 columns 105 / 98,
-// as tiles 116 / 173; 32 rows as 32 columns 107 / 115, as tiles 116 / 162 (and 33 rows would be two column units).
-// Head dim 64: 68 / 72, 70 / 91, 97 / 132; 76 / 101, 94 / 122.  (The mean misjudges one long chunk among single
+// keys, 8 kv heads, head dim 128, bf16 / e4m3 cache, in us: 16 rows as 16 columns 106 / 85, as 32 columns 105 / 101,
+// as tiles 116 / 171; 32 rows as 32 columns 107 / 118, as tiles 115 / 161 (and 33 rows would be two column units).
+// Head dim 64: 70 / 69, 72 / 94, 98 / 131; 78 / 102, 94 / 122.  (The mean misjudges one long chunk among single
 // tokens: right, but as column units that each read the chunk's keys.)
 template <int D, bool KV8>
 cudaError_t launch_attend(const attn_paged_kv_t* c, const PagedParams& p, int max_new, void* workspace, cudaStream_t s) {

@@ -27,18 +27,18 @@
 // of the same MMAs -- half the MMAs of two passes -- and are added in the softmax (the low terms carry a factor of 16).
 // The weights are fp16 and V is turned into fp16, exactly, by four more warps.  Two e4m3 terms per weight would end at
 // 2^-17 of a row's largest, and what falls below is lost with one sign: with one key 13 nats above 8191 others O was
-// 18 % off.  Sixteen warps of six roles fill the instruction cache (120 KB of code); kept small for that are the loading code (one
-// copy for K and V), the conversion (rolled) and the waits (paged_wait), and the scheduler splits q, not the converters:
-// 1.3 stalls for want of an instruction per instruction issued, 4.9 without these.  The issuers are elected, which
-// keeps descriptors uniform (32 rows 127 -> 116 us, D = 64 78 -> 72).
+// 18 % off.  Sixteen warps of six roles fill the instruction cache (120 KB of code).  Kept small for that are the
+// conversion (rolled: 32 rows 124 -> 117 us) and the waits (paged_wait), and the scheduler splits q, not the
+// converters (stalls for want of an instruction 1.4 per instruction issued, 4.9 with q split there).  The issuers are
+// elected, which keeps descriptors uniform (32 rows 127 -> 116 us).
 //
 // Measured (B200, the whole call on the device): 64 sequences of up to 8192 bf16 keys, 8 kv heads of 128, 1.12 GB:
 // 173-180 us, 6.2-6.5 TB/s, bound by DRAM.  4 x 32768 e4m3 keys, 268 MB: 56 us, 4.8 TB/s: 43 us of loads at
 // 6.3 TB/s, the rest is start (planning, first loads: 5 us), end and merge.  One sequence of 2000 keys: 12.3-12.7 us,
 // nearly all of it latency (planning 2 us, first load 1.5, two blocks 3, end 2, merge 3).  e4m3 in many short units is
-// bound by issuing P V: 8 MMAs and their waits take 1200-1500 clk a block, where the loads take 1400 (D = 128) or
-// 700 (D = 64), and a unit's end is not overlapped with the next one's P V (64 sequences of up to 4096 keys: 78 us,
-// D = 64 74 us; loads alone 46 and 23).
+// bound by the chain conversion -> P V (1000-1450 clk a block, where the loads take 1400, or 700 at D = 64), and a
+// unit's end, 3000 clk, is not overlapped with the next one's P V (64 sequences of up to 4096 keys: 78 us,
+// D = 64 65 us; loads alone 46 and 23).
 #pragma once
 
 #include "paged_plan.cuh"
@@ -290,7 +290,7 @@ __global__ void __launch_bounds__(FewLayout<D, KV8, NQ>::THREADS, 1)
         const int s = kn % L::ST;
         const uint32_t ph = ((kn / L::ST) - 1) & 1;
         if (kn >= L::ST && !(ok = __all_sync(0xffffffffu, paged_wait(bar(L::B_K_EMPTY + s), ph, ctl)))) break;
-#pragma unroll 1  // (one copy of the code)
+#pragma unroll
         for (int v = 0; v < (one_loader ? 2 : 1); ++v) {
           if (v == 1 && vn >= L::ST && !(ok = __all_sync(0xffffffffu, paged_wait(bar(L::B_V_EMPTY + s), ph, ctl)))) break;
           load_block<L::NBOX, L::ROW_BYTES>(p, v == 0 ? &tm_k : &tm_v, sbase + (v == 0 ? L::K_OFF : L::V_OFF) + s * L::KV_BYTES,
