@@ -245,8 +245,11 @@ def bwd(q, k, v, o, lse, do, causal: bool = False, scale: float | None = None, d
     return dq, dk, dv
 
 
-def _rotary_lengths(S_q, S_k):
-    if S_q != S_k:
+def _check_rotary(rotary, positions, S_q, S_k):
+    if rotary is None:
+        if positions is not None:
+            raise ValueError("positions are given without rotary")
+    elif S_q != S_k:
         raise ValueError(f"rotary needs S_q == S_k (one position per token), got {S_q} and {S_k}")
 
 
@@ -259,9 +262,8 @@ def fwd_bwd(q, k, v, do, causal: bool = False, scale: float | None = None, host_
     host or device) and dq, dk are the gradients of the unrotated q and k: bwd's bf16 results turned
     back in place, so rounded twice.
     Returns the dict of host results."""
-    if rotary is not None:
-        _shapes(q, k)
-        _rotary_lengths(q.shape[1], k.shape[1])
+    _shapes(q, k)
+    _check_rotary(rotary, positions, q.shape[1], k.shape[1])
     dev = torch.device("cuda", torch.cuda.current_device())
     if stream is not None and stream.device != dev:
         raise ValueError(f"stream is on {stream.device}, the current device is {dev}")
@@ -312,8 +314,7 @@ class FwdBwdPipeline:
 
     def __init__(self, B, S_q, S_k, H_q, H_kv, D, causal: bool = False, scale: float | None = None,
                  depth: int = 2, device=None, rotary: Rotary | None = None, positions=None):
-        if rotary is not None:
-            _rotary_lengths(S_q, S_k)
+        _check_rotary(rotary, positions, S_q, S_k)
         self.rotary, self.positions = rotary, positions
         self.dev = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
         self.causal = bool(causal)

@@ -85,3 +85,12 @@ def test_without_rotation_the_steps_wait_for_nothing_of_the_caller(fake):
     _step(pipe)
     assert [name for name, _ in fake.seen] == ["fwd", "bwd"]
     assert all("something else" not in behind for _, behind in fake.seen)
+
+
+def test_positions_without_rotary_are_refused(fake):
+    positions = torch.zeros((1, 4), dtype=torch.int32)
+    with pytest.raises(ValueError, match="without rotary"):
+        attn.FwdBwdPipeline(1, 4, 4, 1, 1, 64, device="cpu", positions=positions)
+    x = torch.zeros((1, 4, 1, 64), dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="without rotary"):
+        attn.fwd_bwd(x, x, x, x, positions=positions)
