@@ -210,11 +210,16 @@ __device__ __forceinline__ void paged_walk_start(const PagedParams& p, PagedWalk
     b0 += 32;
   }
   const unsigned past = __ballot_sync(0xffffffffu, before + upto > k.at);
-  const int src = past == 0 ? 0 : __ffs(past) - 1;  // (never 0: k.at < total)
+  // Lengths that change while the call runs may make this reading differ from the one that gave `total`: such a
+  // stretch is left out, so that no place outside the tensors follows from it.
+  bool torn = past == 0;
+  const int src = past == 0 ? 0 : __ffs(past) - 1;
   const long long ph = max(1ll, __shfl_sync(0xffffffffu, per_head, src));
   long long r = k.at - before - (__shfl_sync(0xffffffffu, upto, src) - ph * p.H_kv);
   k.b = b0 + src;
-  k.head = static_cast<int>(quotient(r, ph));
+  const long long head = quotient(r, ph);
+  torn |= head >= p.H_kv;
+  k.head = torn ? 0 : static_cast<int>(head);
   r -= ph * k.head;
   k.w.qs = __shfl_sync(0xffffffffu, w.qs, src);
   k.w.n_new = __shfl_sync(0xffffffffu, w.n_new, src);
@@ -237,10 +242,15 @@ __device__ __forceinline__ void paged_walk_start(const PagedParams& p, PagedWalk
       r -= __shfl_sync(0xffffffffu, sum, 31);
       continue;
     }
+    torn |= in == 0;
     const int lu = in == 0 ? 0 : __ffs(in) - 1;
     k.u = u0 + lu;
     k.step = static_cast<int>(r - (__shfl_sync(0xffffffffu, sum, lu) - __shfl_sync(0xffffffffu, steps, lu)));
     break;
+  }
+  if (torn) {
+    if (lane == 0) atomicExch(p.status, kDevBadIndex);
+    k.end = k.at;
   }
 }
 
@@ -305,7 +315,8 @@ __device__ __forceinline__ int4 paged_cut(const PagedParams& p, const PagedWalk&
   if (start < (cta - 1) * k.per) return make_int4(-1, 0, 0, 0);
   const int q0 = k.u * p.unit_pos;
   const long long last = quotient(start + unit_steps(p, k.w, k.u, k.as) - 1, k.per);
-  return make_int4(k.w.qs + q0, min(p.unit_pos, k.w.n_new - q0), k.head, static_cast<int>(last));
+  const long long end = static_cast<long long>(gridDim.x) - 1;  // (`last` is beyond only where lengths change meanwhile)
+  return make_int4(k.w.qs + q0, min(p.unit_pos, k.w.n_new - q0), k.head, static_cast<int>(min(last, end)));
 }
 
 // Joins the pieces of the units that were cut.  Block (c, y): rows 8 y .. 8 y + 7 of the unit

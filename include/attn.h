@@ -261,7 +261,7 @@ attn_status_t attn_rope(const void* q, const void* k, void* q_out, void* k_out, 
  *                 keys.  A sequence may have none.  Rows before q_start[0] and from q_start[n_seq]
  *                 on are left as they were in every output.
  * The three index arrays are read on the device when the call runs (a captured call
- * reads their contents at replay).  Entries that lead outside the cache -- a page not in
+ * reads their contents at replay); where they change meanwhile the call's results are undefined, its accesses in range.  Entries that lead outside the cache -- a page not in
  * [0, n_pages) among those a sequence needs, a length beyond max_pages * page_size,
  * more new tokens than keys in an append, a token range outside [0, n_tokens] or running backwards -- never cause an
  * access out of range: the call records ATTN_ERR_BAD_INDEX in the device status word and the

@@ -581,6 +581,47 @@ def test_handles_follow_their_tensors_or_refuse():
             setattr(r, name, value)
 
 
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("hint", [1, 20, 400])
+def test_lengths_that_change_meanwhile(hint, e4m3):
+    """Another stream rewrites lengths and ranges, each content valid, while calls run: nothing outside the outputs and
+    the workspace is written, and a call on settled lengths is right again."""
+    attn = _attn()
+    rng = np.random.default_rng(5)
+    B = 150
+    new = [int(n) for n in rng.choice([1, 2, 9, 40], B)]
+    x = make(new, [n + int(k) for n, k in zip(new, rng.integers(300, 900, B))], 4, 2, 64, 64, e4m3=e4m3, seed=31, poison=False)
+    g = to_gpu(x)
+    g["page_table"].clamp_(max=x["k_cache"].shape[0] - 1)
+    T = sum(new)
+    size = attn.fwd_paged_workspace_size(4, 2, 64)
+    out = torch.full((T + 64, 4, 64), 7.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((4 * T + 128,), 7.0, device="cuda")
+    ws = torch.full((size + 65536,), 7, dtype=torch.uint8, device="cuda")
+    o, l, w = out[32:32 + T], lse[64:64 + 4 * T].view(4, T), ws[32768:32768 + size]
+    cache = handle(attn, g)
+    want = attn.fwd_paged(cache, g["q"], max_new=hint)
+    lens, starts = g["seq_len"].clone(), g["q_start"].clone()
+    other = torch.tensor(sorted(rng.integers(0, T + 1, B + 1).tolist()), dtype=torch.int32, device="cuda")
+    short = torch.tensor(rng.integers(0, 300, B), dtype=torch.int32, device="cuda")
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        for i in range(400):
+            g["seq_len"].copy_(short if i % 2 == 0 else lens)
+            g["q_start"].copy_(other if i % 3 == 0 else starts)
+    for _ in range(40):
+        attn.fwd_paged(cache, g["q"], max_new=hint, out=o, lse=l, workspace=w)
+    torch.cuda.synchronize()
+    assert attn.device_status() in (0, 7)
+    for t, a, b, v in ((out, 32, 32 + T, 7.0), (lse, 64, 64 + 4 * T, 7.0), (ws, 32768, 32768 + size, 7)):
+        assert bool((t[:a] == v).all()) and bool((t[b:] == v).all())
+    g["seq_len"].copy_(lens)
+    g["q_start"].copy_(starts)
+    again = attn.fwd_paged(cache, g["q"], max_new=hint, out=o, lse=l, workspace=w)
+    assert torch.equal(again[0], want[0]) and torch.equal(again[1], want[1]) and attn.device_status() == 0
+
+
 @pytest.mark.parametrize("length", [-1, 33, 2 ** 31 - 1])
 def test_bad_lengths_without_rows_are_reported(length):
     attn = _attn()
